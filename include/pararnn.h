@@ -427,6 +427,109 @@ pararnn_status_t pararnn_solve_gru_noalloc(const void* P, pararnn_dtype_t p_dtyp
 pararnn_status_t pararnn_probe_rate(int32_t pipe, int32_t iters, float* sink, int64_t* ops,
                                     void* stream);
 
+/* Linear attention with one decay per head: an affine scan whose state is a
+ * Dk x Dv matrix per (batch row, head), written by k and v and read by q.  It
+ * stands beside the scalar and 2x2 scans (pararnn_scan_diag / _block2) as the
+ * mixing layer whose recurrence is linear (the pages have no counterpart).
+ *   S_t = gamma_h S_{t-1} + k_t^T v_t,  o_t = scale q_t S_t,  t = 1..n_b,
+ *   gamma_h = exp(log_decay[h]),  n_b = min(max(lengths[b], 0), L) or L.
+ * A log decay of -inf is gamma = 0 (each token sees itself only), 0 is gamma = 1.
+ *
+ * Shapes of a call (host struct):
+ *  B, L       : batch rows and tokens.     H : heads (decays, states, outputs).
+ *  Hq, Hk, Hv : heads of q, k and v, each dividing H: head h of the call reads
+ *               head h / (H / Hx) of a stream, and a stream's gradient is the
+ *               sum over the heads that share it.
+ *  Dk, Dv     : head sizes of q, k and of v, o: multiples of 8 up to 128.
+ *  x_stride   : element strides (batch, token, head) of q, k, v and do, whose last
+ *               axis is contiguous, so that views of one packed projection can
+ *               be passed as they are.  Scan and backward need positive strides
+ *               that are multiples of 8 and 16-byte aligned streams (give an axis of
+ *               size 1 any such stride); the step takes any strides >= 0. */
+typedef struct {
+  int64_t B, L;
+  int32_t H, Hq, Hk, Hv, Dk, Dv;
+  float scale;
+  int32_t reserved;
+  int64_t q_stride[3], k_stride[3], v_stride[3], do_stride[3];
+} pararnn_linattn_t;
+
+/* Workspace bytes of pararnn_scan_linattn (backward = 0) or its backward pass
+ * (backward = 1) for these shapes; strides and scale do not matter.  0 on bad
+ * sizes. */
+size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* desc, int32_t backward);
+
+/* The scan over a prompt.
+ *  q [B, L, Hq, Dk], k [B, L, Hk, Dk], v [B, L, Hv, Dv]: bf16, strided as above.
+ *  log_decay [H] fp32.    s0 [B, H, Dk, Dv] fp32 or NULL (= 0).
+ *  lengths [B] int32 in DEVICE memory or NULL: tokens at and after a row's length
+ *  are not used, whatever they hold, and their rows of o are left as they were.
+ *  o [B, L, H, Dv] bf16.   s [B, H, Dk, Dv] fp32: the state after the last token,
+ *  or NULL; s may be s0 itself.
+ *  ws, ws_bytes: workspace of pararnn_linattn_workspace_size(desc, 0) bytes.
+ *  status_dev: optional device int32 for the device-side status.
+ * A non-finite v makes the whole state's column non-finite from its token on, as the
+ * formula says; see the note on chunks in the source for the tokens before it.
+ * Errors: PARARNN_ERR_INVALID_ARGUMENT, _WORKSPACE, _UNSUPPORTED, _CUDA. */
+pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* desc, const void* q, const void* k,
+                                      const void* v, const float* log_decay, const float* s0,
+                                      const int32_t* lengths, void* o, float* s, void* ws,
+                                      size_t ws_bytes, int32_t* status_dev,
+                                      const pararnn_options_t* opts, void* stream);
+
+/* Gradients of a loss through that scan.  dout = dl/do [B, L, H, Dv] bf16 (strided,
+ * do_stride), ds = dl/ds [B, H, Dk, Dv] fp32 of the final state or NULL (= 0).
+ *   dq_t = scale do_t S_t^T,  R_t = gamma R_{t+1} + scale q_t^T do_t,
+ *   dk_t = v_t R_t^T,  dv_t = k_t R_t,  ds0 = gamma R_1,
+ * with gamma R_{n+1} read as ds.  The decay is a constant of the layer: it gets
+ * no gradient.
+ *  dq [B, L, Hq, Dk], dk [B, L, Hk, Dk], dv [B, L, Hv, Dv]: bf16, contiguous; rows at
+ *  and after a batch row's length are set to zero.  ds0 [B, H, Dk, Dv] fp32 or NULL;
+ *  it must not overlap ds.  ws: pararnn_linattn_workspace_size(desc, 1) bytes. */
+pararnn_status_t pararnn_scan_linattn_backward(
+    const pararnn_linattn_t* desc, const void* q, const void* k, const void* v,
+    const float* log_decay, const float* s0, const void* dout, const float* ds,
+    const int32_t* lengths, void* dq, void* dk, void* dv, float* ds0, void* ws, size_t ws_bytes,
+    int32_t* status_dev, const pararnn_options_t* opts, void* stream);
+
+/* One token of that recurrence (the decode step): s_next = gamma s_prev + k^T v,
+ * o = scale q s_next.  desc->L must be 1; the strides' token entry is not used.
+ *  q [B, Hq, Dk], k [B, Hk, Dk], v [B, Hv, Dv], o [B, H, Dv] (contiguous): all fp32 or
+ *  all bf16 (dtype).  s_prev [B, H, Dk, Dv] fp32 or NULL (= 0); s_next the same
+ *  shape and may be s_prev itself (a state cache updated in place). */
+pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* desc, const void* q, const void* k,
+                                      const void* v, pararnn_dtype_t dtype,
+                                      const float* log_decay, const float* s_prev, void* o,
+                                      float* s_next, void* stream);
+
+/* Layer norm over the last axis: what stands between two recurrent layers (the
+ * solves give fp32 h, the projections read bf16 x) and, on rows of one head,
+ * behind linear attention (the pages have no counterpart).
+ *   y = (x - mean) rstd weight + bias,  rstd = (var + eps)^(-1/2)
+ *  x [M, D] fp32 or bf16, rows x_stride elements apart (last axis contiguous);
+ *  weight, bias [D] fp32 or NULL (1 and 0);  y [M, D] fp32 or bf16, contiguous;
+ *  mean, rstd [M] fp32: the rows' statistics, which the backward pass reads.
+ *  eps >= 0.  Statistics are fp32, the variance is taken about the mean.  */
+pararnn_status_t pararnn_layer_norm(const void* x, pararnn_dtype_t x_dtype, int64_t x_stride,
+                                    const float* weight, const float* bias, void* y,
+                                    pararnn_dtype_t y_dtype, float* mean, float* rstd, int64_t M,
+                                    int64_t D, float eps, void* stream);
+
+/* Workspace bytes of the layer norm's backward pass.  0 on bad sizes. */
+size_t pararnn_layer_norm_workspace_size(int64_t M, int64_t D);
+
+/* Its gradients: with g = dy weight and xh = (x - mean) rstd,
+ *   dx = rstd (g - mean(g) - xh mean(g xh)),  dweight = sum dy xh,  dbias = sum dy,
+ * the sums over the M rows joined in a fixed order (the same bits every call).
+ *  dy [M, D] fp32 or bf16 with row stride dy_stride;  dx [M, D] of x's type,
+ *  contiguous;  dweight, dbias [D] fp32 (overwritten; zero for M = 0).
+ *  ws: pararnn_layer_norm_workspace_size(M, D) bytes, 256-byte aligned. */
+pararnn_status_t pararnn_layer_norm_backward(
+    const void* dy, pararnn_dtype_t dy_dtype, int64_t dy_stride, const void* x,
+    pararnn_dtype_t x_dtype, int64_t x_stride, const float* weight, const float* mean,
+    const float* rstd, void* dx, float* dweight, float* dbias, int64_t M, int64_t D, void* ws,
+    size_t ws_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* pararnn_status_string(pararnn_status_t status);
 

@@ -18,6 +18,10 @@ Entry points (same names as the C ABI, without the ``pararnn_`` prefix):
 * ``input_projection(x, W, bias=None)``  P = x W^T + bias on the tensor cores
 * ``solve_gru_projected(x, W, bias, a, h0=None)``  the projection fused with the
   ParaGRU Newton solve (P never reaches HBM)
+* ``scan_linattn(q, k, v, log_decay, s0=None)``  linear attention with one decay per
+  head over a prompt;  ``scan_linattn_backward``  its gradients;  ``step_linattn``
+  one token
+* ``layer_norm(x, weight, bias)`` / ``layer_norm_backward``  layer norm and its gradients
 * ``step_gru`` / ``step_lstm``      one decode step;  ``rollout_gru`` / ``rollout_lstm``
   the sequential application on the GPU
 
@@ -37,6 +41,8 @@ from . import build as _build
 __all__ = ["scan_diag", "scan_block2", "solve_gru", "solve_lstm", "solve_gru_noalloc", "solve_gru_projected", "solve_mhgru_strided",
            "solve_gru_backward", "solve_lstm_backward", "solve_mhgru", "input_projection",
            "step_gru", "step_lstm", "rollout_gru", "rollout_lstm",
+           "scan_linattn", "scan_linattn_backward", "step_linattn",
+           "layer_norm", "layer_norm_backward",
            "workspace_size", "probe_rate", "PROBE_MUFU", "PROBE_FMA",
            "SolveInfo", "Options", "PararnnError", "library_path", "load", "MAX_ITERS"]
 
@@ -82,6 +88,16 @@ class Options(ctypes.Structure):
                  regime=0, walk_warps=0, walk_width=0):
         super().__init__(iters_first, iters_next, wait_timeout_ns, debug_stall_unit, regime,
                          walk_warps, walk_width, 0)
+
+
+class _LinAttn(ctypes.Structure):
+    """Shapes and strides of a linear-attention call (see pararnn_linattn_t)."""
+    _fields_ = [("B", ctypes.c_int64), ("L", ctypes.c_int64), ("H", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("Hv", ctypes.c_int32),
+                ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("do_stride", ctypes.c_int64 * 3)]
 
 
 INFO_BYTES = ctypes.sizeof(_Info)
@@ -168,6 +184,24 @@ def load(build_if_missing: bool = True):
             lib.pararnn_solve_gru_projected.restype = ctypes.c_int
             lib.pararnn_probe_rate.argtypes = [ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp]
             lib.pararnn_probe_rate.restype = ctypes.c_int
+            _sz, _i32, _f = ctypes.c_size_t, ctypes.c_int32, ctypes.c_float
+            lib.pararnn_linattn_workspace_size.argtypes = [_vp, _i32]
+            lib.pararnn_linattn_workspace_size.restype = _sz
+            lib.pararnn_scan_linattn.argtypes = [_vp] * 10 + [_sz, _vp, _vp, _vp]
+            lib.pararnn_scan_linattn.restype = ctypes.c_int
+            lib.pararnn_scan_linattn_backward.argtypes = [_vp] * 14 + [_sz, _vp, _vp, _vp]
+            lib.pararnn_scan_linattn_backward.restype = ctypes.c_int
+            lib.pararnn_step_linattn.argtypes = [_vp] * 4 + [ctypes.c_int] + [_vp] * 5
+            lib.pararnn_step_linattn.restype = ctypes.c_int
+            lib.pararnn_layer_norm.argtypes = [_vp, ctypes.c_int, _i64, _vp, _vp, _vp,
+                                               ctypes.c_int, _vp, _vp, _i64, _i64, _f, _vp]
+            lib.pararnn_layer_norm.restype = ctypes.c_int
+            lib.pararnn_layer_norm_workspace_size.argtypes = [_i64, _i64]
+            lib.pararnn_layer_norm_workspace_size.restype = _sz
+            lib.pararnn_layer_norm_backward.argtypes = [_vp, ctypes.c_int, _i64, _vp,
+                                                        ctypes.c_int, _i64] + [_vp] * 6 + \
+                                                       [_i64, _i64, _vp, _sz, _vp]
+            lib.pararnn_layer_norm_backward.restype = ctypes.c_int
             lib.pararnn_status_string.argtypes = [ctypes.c_int]
             lib.pararnn_status_string.restype = ctypes.c_char_p
             lib.pararnn_version.restype = ctypes.c_int32
@@ -820,6 +854,275 @@ def rollout_lstm(P, a, c0=None, h0=None, out=None, stream=None):
                                       B, L, D, _stream_handle(stream, dev))
     _raise(st, "pararnn_rollout_lstm")
     return c, h
+
+
+def _stream_tensor(name, t, dtype, shape, unit):
+    """Checks one stream of a linear-attention call and returns its element
+    strides.  The last axis is contiguous; with ``unit`` > 1 every stride is a
+    positive multiple of it and the first element is aligned to it (what the
+    tensor copies need).  An axis of size 1 takes the stride of a dense layout."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    strides = []
+    dense = t.shape[-1]
+    if t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        strides.append(st if n > 1 else dense)
+        dense *= max(n, 1)
+        if unit > 1 and n > 1 and t.numel() > 0 and (st <= 0 or st % unit):
+            raise ValueError(f"{name}: strides must be positive multiples of {unit} elements, "
+                             f"got {tuple(t.stride())}")
+    if unit > 1 and t.data_ptr() % (unit * t.element_size()):
+        raise ValueError(f"{name} must start on a {unit * t.element_size()}-byte boundary")
+    return strides[::-1]
+
+
+def _linattn_shapes(q, k, v, log_decay, scale, dtype, unit, tokens):
+    """The call's descriptor from its tensors ([B, L, heads, size], or [B, heads,
+    size] for one token)."""
+    nd = 4 if tokens else 3
+    if q.dim() != nd or k.dim() != nd or v.dim() != nd or log_decay.dim() != 1:
+        raise ValueError("q, k, v must be [B, L, heads, size] and log_decay [H]" if tokens else
+                         "q, k, v must be [B, heads, size] and log_decay [H]")
+    lead = tuple(q.shape[:-2])
+    Hq, Dk = q.shape[-2:]
+    Hk, (Hv, Dv), H = k.shape[-2], v.shape[-2:], log_decay.shape[0]
+    if H == 0 or min(Hq, Hk, Hv) == 0 or H % Hq or H % Hk or H % Hv:
+        raise ValueError(f"the heads of q, k and v ({Hq}, {Hk}, {Hv}) must divide the {H} heads "
+                         "of log_decay")
+    if Dk % 8 or Dv % 8 or not 8 <= Dk <= 128 or not 8 <= Dv <= 128:
+        raise ValueError(f"head sizes must be multiples of 8 from 8 to 128, got {Dk} and {Dv}")
+    d = _LinAttn(B=lead[0], L=lead[1] if tokens else 1, H=H, Hq=Hq, Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv,
+                 scale=float(scale))
+    for name, t, h, n in (("q", q, Hq, Dk), ("k", k, Hk, Dk), ("v", v, Hv, Dv)):
+        st = _stream_tensor(name, t, dtype, lead + (h, n), unit)
+        getattr(d, name + "_stride")[:] = st if tokens else [st[0], 0, st[1]]
+    _check_dev("log_decay", log_decay, torch.float32, (H,))
+    return d
+
+
+def _call_buffer(nbytes, device, stream):
+    """Workspace of one call, from torch's allocator for the stream it runs on.
+    Taken anew each call, so that captured graphs keep workspaces of their own."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _overlap(a, b):
+    """Whether two dense tensors share any byte."""
+    x, y = a.data_ptr(), b.data_ptr()
+    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+
+
+def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None, state_out=None,
+                 status=None, opts: Options | None = None, stream=None):
+    """Linear attention with one decay per head over a prompt:
+    S_t = exp(log_decay) S_{t-1} + k_t^T v_t, o_t = scale q_t S_t.
+
+    q [B, L, Hq, Dk], k [B, L, Hk, Dk], v [B, L, Hv, Dv] bf16 (strided views allowed,
+    last axis contiguous), log_decay [H] fp32, s0 [B, H, Dk, Dv] fp32 or None ->
+    (o [B, L, H, Dv] bf16, s [B, H, Dk, Dv] fp32).  lengths [B] int32 (device): tokens
+    at and after a row's length are not used; their rows of o are left as they were
+    in ``out`` and are zero in a tensor this call makes.  ``state_out`` may be s0."""
+    lib = load()
+    d = _linattn_shapes(q, k, v, log_decay, scale, torch.bfloat16, 8, True)
+    B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
+    _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
+    _check_dev("lengths", lengths, torch.int32, (B,))
+    if out is None:
+        make = torch.empty if lengths is None else torch.zeros
+        out = make((B, L, H, Dv), dtype=torch.bfloat16, device=q.device)
+    if state_out is None:
+        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    elif s0 is not None and state_out.data_ptr() != s0.data_ptr() and _overlap(state_out, s0):
+        raise ValueError("state_out must be s0 itself or not overlap it")
+    _check_dev("out", out, torch.bfloat16, (B, L, H, Dv))
+    _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
+    _check_dev("status", status, torch.int32, (1,))
+    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s0=s0, lengths=lengths, out=out,
+                      state_out=state_out, status=status)
+    ws = _call_buffer(lib.pararnn_linattn_workspace_size(ctypes.byref(d), 0), dev, stream)
+    with _device_guard(dev):
+        st = lib.pararnn_scan_linattn(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                      _ptr(s0), _ptr(lengths), _ptr(out), _ptr(state_out),
+                                      _ptr(ws), ws.numel(), _ptr(status),
+                                      ctypes.byref(opts) if opts is not None else None,
+                                      _stream_handle(stream, dev))
+    _raise(st, "pararnn_scan_linattn")
+    return out, state_out
+
+
+def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, lengths=None,
+                          out=None, status=None, opts: Options | None = None, stream=None):
+    """Gradients of a loss through ``scan_linattn``, given do = dl/do [B, L, H, Dv] bf16
+    and ds = dl/ds of the final state (or None): (dq, dk, dv bf16 in the shapes of q, k
+    and v, summed over the heads that share one; ds0 [B, H, Dk, Dv] fp32).  Rows at and
+    after a batch row's length get zeros.  The decay is a constant of the layer."""
+    lib = load()
+    d = _linattn_shapes(q, k, v, log_decay, scale, torch.bfloat16, 8, True)
+    B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
+    d.do_stride[:] = _stream_tensor("do", do, torch.bfloat16, (B, L, H, Dv), 8)
+    _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
+    _check_dev("ds", ds, torch.float32, (B, H, Dk, Dv))
+    _check_dev("lengths", lengths, torch.int32, (B,))
+    if out is None:
+        dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
+                      for t in (q, k, v))
+        ds0 = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    else:
+        dq, dk, dv, ds0 = out
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_dev(name, t, torch.bfloat16, like.shape)
+    _check_dev("ds0", ds0, torch.float32, (B, H, Dk, Dv))
+    if ds is not None and _overlap(ds, ds0):
+        raise ValueError("ds0 must not overlap ds")
+    _check_dev("status", status, torch.int32, (1,))
+    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
+                      dq=dq, dk=dk, dv=dv, ds0=ds0, status=status)
+    ws = _call_buffer(lib.pararnn_linattn_workspace_size(ctypes.byref(d), 1), dev, stream)
+    with _device_guard(dev):
+        st = lib.pararnn_scan_linattn_backward(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(s0), _ptr(do),
+            _ptr(ds), _ptr(lengths), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(ws),
+            ws.numel(), _ptr(status), ctypes.byref(opts) if opts is not None else None,
+            _stream_handle(stream, dev))
+    _raise(st, "pararnn_scan_linattn_backward")
+    return dq, dk, dv, ds0
+
+
+def step_linattn(q, k, v, log_decay, s_prev=None, scale=1.0, out=None, state_out=None,
+                 stream=None):
+    """One token of linear attention (decode): s = exp(log_decay) s_prev + k^T v,
+    o = scale q s.  q [B, Hq, Dk], k [B, Hk, Dk], v [B, Hv, Dv] all fp32 or all bf16
+    (last axis contiguous), s_prev [B, H, Dk, Dv] fp32 or None -> (o [B, H, Dv] of
+    their type, s).  ``state_out`` may be s_prev: the state is then updated in place."""
+    lib = load()
+    dt = F32 if q.dtype == torch.float32 else BF16
+    if q.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
+    d = _linattn_shapes(q, k, v, log_decay, scale, q.dtype, 1, False)
+    B, H, Dk, Dv = d.B, d.H, d.Dk, d.Dv
+    _check_dev("s_prev", s_prev, torch.float32, (B, H, Dk, Dv))
+    if out is None:
+        out = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
+    if state_out is None:
+        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    elif s_prev is not None and state_out.data_ptr() != s_prev.data_ptr() \
+            and _overlap(state_out, s_prev):
+        raise ValueError("state_out must be s_prev itself or not overlap it")
+    _check_dev("out", out, q.dtype, (B, H, Dv))
+    _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
+    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s_prev=s_prev, out=out,
+                      state_out=state_out)
+    with _device_guard(dev):
+        st = lib.pararnn_step_linattn(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), dt,
+                                      _ptr(log_decay), _ptr(s_prev), _ptr(out), _ptr(state_out),
+                                      _stream_handle(stream, dev))
+    _raise(st, "pararnn_step_linattn")
+    return out, state_out
+
+
+def _norm_dtype(name, t):
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows(name, t):
+    """(rows, row stride) of a tensor whose last axis is contiguous and whose
+    leading axes are evenly spaced rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() == 0 or t.shape[-1] == 0:
+        raise ValueError(f"{name} must have a last axis of at least one element")
+    if t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    rows, stride = 1, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n > 1 and rows > 0:
+            if stride is None:
+                stride = st
+            elif st != stride * rows:
+                raise ValueError(f"{name}: the leading axes must be evenly spaced rows, got "
+                                 f"strides {tuple(t.stride())}")
+        rows *= n
+    return rows, t.shape[-1] if stride is None else stride
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, stats=None,
+               stream=None):
+    """Layer norm over the last axis: y = (x - mean) rstd weight + bias.
+
+    x [..., D] fp32 or bf16 (evenly spaced rows), weight and bias [D] fp32 or None ->
+    (y [..., D] of out_dtype (x's by default), mean [...], rstd [...] fp32, which
+    ``layer_norm_backward`` reads).  out_dtype=torch.bfloat16 on a solve's fp32 h gives
+    the next projection's input."""
+    lib = load()
+    dx = _norm_dtype("x", x)
+    M, sx = _rows("x", x)
+    D, lead = x.shape[-1], tuple(x.shape[:-1])
+    _check_dev("weight", weight, torch.float32, (D,))
+    _check_dev("bias", bias, torch.float32, (D,))
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    y = torch.empty(x.shape, dtype=out_dtype, device=x.device) if out is None else out
+    _check_dev("out", y, out_dtype, x.shape)
+    mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2)) \
+        if stats is None else stats
+    _check_dev("mean", mean, torch.float32, lead)
+    _check_dev("rstd", rstd, torch.float32, lead)
+    dev = _one_device(x=x, weight=weight, bias=bias, out=y, mean=mean, rstd=rstd)
+    with _device_guard(dev):
+        st = lib.pararnn_layer_norm(_ptr(x), dx, sx, _ptr(weight), _ptr(bias), _ptr(y),
+                                    BF16 if out_dtype == torch.bfloat16 else F32, _ptr(mean),
+                                    _ptr(rstd), M, D, float(eps), _stream_handle(stream, dev))
+    _raise(st, "pararnn_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
+    """Gradients of a loss through ``layer_norm``, given dy = dl/dy (fp32 or bf16, x's
+    shape) and the mean and rstd it returned: (dx of x's type, dweight [D], dbias [D]
+    fp32).  The weight's gradient is summed in a fixed order."""
+    lib = load()
+    tx, ty = _norm_dtype("x", x), _norm_dtype("dy", dy)
+    M, sx = _rows("x", x)
+    if tuple(dy.shape) != tuple(x.shape):
+        raise ValueError(f"dy: expected shape {tuple(x.shape)}, got {tuple(dy.shape)}")
+    _, sdy = _rows("dy", dy)
+    D, lead = x.shape[-1], tuple(x.shape[:-1])
+    _check_dev("weight", weight, torch.float32, (D,))
+    _check_dev("mean", mean, torch.float32, lead)
+    _check_dev("rstd", rstd, torch.float32, lead)
+    if out is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw, db = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
+    else:
+        dx, dw, db = out
+    _check_dev("dx", dx, x.dtype, x.shape)
+    _check_dev("dweight", dw, torch.float32, (D,))
+    _check_dev("dbias", db, torch.float32, (D,))
+    dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dw,
+                      dbias=db)
+    ws = _call_buffer(lib.pararnn_layer_norm_workspace_size(M, D), dev, stream)
+    with _device_guard(dev):
+        st = lib.pararnn_layer_norm_backward(_ptr(dy), ty, sdy, _ptr(x), tx, sx, _ptr(weight),
+                                             _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
+                                             _ptr(db), M, D, _ptr(ws), ws.numel(),
+                                             _stream_handle(stream, dev))
+    _raise(st, "pararnn_layer_norm_backward")
+    return dx, dw, db
 
 
 PROBE_MUFU, PROBE_FMA = 0, 1

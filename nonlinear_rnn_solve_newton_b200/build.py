@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -12,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpararnn.so")
-SOURCES = [os.path.join(CSRC, "pararnn.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("pararnn.cu", "linattn.cu", "norm.cu")]
 DEPS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "pararnn.h")]
 
 
@@ -30,16 +31,50 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in DEPS)
 
 
+def _includes(path, seen=None):
+    """The file and the project files it includes, directly or not."""
+    seen = set() if seen is None else seen
+    if path not in seen:
+        seen.add(path)
+        with open(path, encoding="utf-8") as f:
+            names = re.findall(r'^\s*#include\s+"([^"]+)"', f.read(), flags=re.M)
+        for n in names:
+            for d in (CSRC, INCLUDE):
+                if os.path.exists(os.path.join(d, n)):
+                    _includes(os.path.join(d, n), seen)
+    return seen
+
+
+def _object(src):
+    return os.path.join(HERE, "_build", os.path.basename(src) + ".o")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-           "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-I" + INCLUDE, "-I" + CSRC,
-           *SOURCES, "-o", LIB + ".tmp"]
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+             "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
+        flags.insert(0, "-Xptxas=-v")
+    os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
+    jobs = []
+    for src in SOURCES:  # the sources that changed, side by side
+        obj = _object(src)
+        if not force and os.path.exists(obj):
+            t = os.path.getmtime(obj)
+            if all(os.path.getmtime(p) <= t for p in _includes(src)):
+                continue
+        cmd = [nvcc_path(), *flags, "-c", src, "-o", obj + ".tmp"]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        jobs.append((cmd, obj, subprocess.Popen(cmd)))
+    failed = [(cmd, rc) for cmd, _, job in jobs if (rc := job.wait()) != 0]
+    if failed:
+        raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+    for _, obj, _ in jobs:
+        os.replace(obj + ".tmp", obj)
+    subprocess.check_call([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
+                           *[_object(s) for s in SOURCES], "-o", LIB + ".tmp"])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -1,0 +1,271 @@
+// linattn.cu -- C ABI of the linear-attention operators (declared in
+// include/pararnn.h): argument validation, workspace layout and launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "pararnn.h"
+#include "pararnn_linattn.cuh"
+
+namespace pararnn {
+namespace {
+
+bool la_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+size_t la_round(size_t n) { return (n + 255) / 256 * 256; }
+
+bool la_sizes_ok(const pararnn_linattn_t* d) {
+  if (!d || d->B < 0 || d->L < 0 || d->H <= 0 || d->Hq <= 0 || d->Hk <= 0 || d->Hv <= 0)
+    return false;
+  if (d->H % d->Hq || d->H % d->Hk || d->H % d->Hv) return false;
+  if (d->Dk <= 0 || d->Dv <= 0 || d->Dk % 8 || d->Dv % 8 || d->Dk > kLaMaxDim || d->Dv > kLaMaxDim)
+    return false;
+  if (d->L >= (1LL << 31) - 256 || d->B > (1LL << 31) - 1 || d->H > (1 << 20)) return false;
+  if (d->B * d->H >= (1LL << 31) - 1) return false;
+  return std::isfinite(d->scale);
+}
+
+// Strides of a stream: tensor copies need whole 16-byte units (8 bf16).
+bool la_strides_ok(const int64_t* s) {
+  for (int i = 0; i < 3; ++i)
+    if (s[i] <= 0 || s[i] % 8 || s[i] >= (1LL << 38)) return false;
+  return true;
+}
+
+LaIn la_in(const void* p, const int64_t* s, int H, int Hx) {
+  return LaIn{p, s[0], s[1], s[2], H / Hx};
+}
+
+pararnn_status_t la_launch_recurrent(const LaParams& lp, bool bf16, cudaStream_t st) {
+  int dv = 0;
+  for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
+  const dim3 grid((unsigned)((long long)lp.B * lp.H), (unsigned)((dv + 31) / 32),
+                  (unsigned)lp.npass);
+  if (bf16)
+    pararnn_linattn_recurrent_kernel<__nv_bfloat16><<<grid, kLaRecThreads, 0, st>>>(lp);
+  else
+    pararnn_linattn_recurrent_kernel<float><<<grid, kLaRecThreads, 0, st>>>(lp);
+  return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
+}
+
+// Workspace: fp32 per-head gradients of the streams whose heads are shared.
+struct LaWs {
+  size_t dq, dk, dv, total;
+};
+LaWs la_ws(const pararnn_linattn_t* d, bool backward) {
+  LaWs w = {};
+  size_t at = 0;
+  const size_t rows = (size_t)d->B * (size_t)d->L * (size_t)d->H;
+  if (backward) {
+    w.dq = at;
+    if (d->Hq != d->H) at += la_round(rows * d->Dk * 4);
+    w.dk = at;
+    if (d->Hk != d->H) at += la_round(rows * d->Dk * 4);
+    w.dv = at;
+    if (d->Hv != d->H) at += la_round(rows * d->Dv * 4);
+  }
+  w.total = at ? at : 256;
+  return w;
+}
+
+pararnn_status_t la_group(const float* x, void* y, const pararnn_linattn_t* d, int Hx, int D,
+                          cudaStream_t st) {
+  const long long rows = d->B * d->L;
+  const long long n = rows * Hx * (D / 4);
+  long long blocks = (n + 255) / 256;
+  if (blocks > 148 * 16) blocks = 148 * 16;
+  pararnn_linattn_group_kernel<<<(unsigned)blocks, 256, 0, st>>>(
+      x, static_cast<__nv_bfloat16*>(y), rows, d->H, Hx, D);
+  return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
+}
+
+// L = 0: the state passes through unchanged.
+pararnn_status_t la_copy_state(const float* s0, float* s, size_t n, cudaStream_t st) {
+  if (!s || s == s0 || n == 0) return PARARNN_OK;
+  const cudaError_t e = s0 ? cudaMemcpyAsync(s, s0, n * 4, cudaMemcpyDeviceToDevice, st)
+                           : cudaMemsetAsync(s, 0, n * 4, st);
+  return e == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace pararnn
+
+using namespace pararnn;
+
+extern "C" size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* d, int32_t backward) {
+  if (!la_sizes_ok(d)) return 0;
+  return la_ws(d, backward != 0).total;
+}
+
+extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, const void* q,
+                                                 const void* k, const void* v,
+                                                 const float* log_decay, const float* s0,
+                                                 const int32_t* lengths, void* o, float* s,
+                                                 void* ws, size_t ws_bytes, int32_t* status_dev,
+                                                 const pararnn_options_t* opts, void* stream) {
+  if (!la_sizes_ok(d)) return PARARNN_ERR_INVALID_ARGUMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->B > 0 && d->L > 0) {
+    if (!q || !k || !v || !o || !log_decay) return PARARNN_ERR_INVALID_ARGUMENT;
+    if (!la_strides_ok(d->q_stride) || !la_strides_ok(d->k_stride) || !la_strides_ok(d->v_stride))
+      return PARARNN_ERR_INVALID_ARGUMENT;
+    if (!la_aligned(q, 16) || !la_aligned(k, 16) || !la_aligned(v, 16) || !la_aligned(o, 16) ||
+        !la_aligned(log_decay, 4) || !la_aligned(lengths, 4))
+      return PARARNN_ERR_INVALID_ARGUMENT;
+  }
+  if (!la_aligned(s0, 16) || !la_aligned(s, 16)) return PARARNN_ERR_INVALID_ARGUMENT;
+  const LaWs w = la_ws(d, false);
+  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
+  (void)opts;
+  if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
+    return PARARNN_ERR_CUDA;
+  if (d->B == 0) return PARARNN_OK;
+  if (d->L == 0)
+    return la_copy_state(s0, s, (size_t)d->B * d->H * d->Dk * d->Dv, st);
+
+  LaParams lp = {};
+  lp.npass = 1;
+  lp.log_decay = log_decay;
+  lp.lengths = lengths;
+  lp.B = (int)d->B;
+  lp.H = d->H;
+  lp.L = d->L;
+  LaPass& a = lp.pass[0];
+  a.q = la_in(q, d->q_stride, d->H, d->Hq);
+  a.k = la_in(k, d->k_stride, d->H, d->Hk);
+  a.v = la_in(v, d->v_stride, d->H, d->Hv);
+  a.o = o;
+  a.oh = d->Dv;
+  a.ot = (long long)d->H * d->Dv;
+  a.ob = a.ot * d->L;
+  a.s_in = s0;
+  a.s_out = s;
+  a.s_r = d->Dv;
+  a.s_c = 1;
+  a.dk = d->Dk;
+  a.dv = d->Dv;
+  a.c_out = d->scale;
+  a.c_kv = 1.0f;
+  return la_launch_recurrent(lp, true, st);
+}
+
+extern "C" pararnn_status_t pararnn_scan_linattn_backward(
+    const pararnn_linattn_t* d, const void* q, const void* k, const void* v,
+    const float* log_decay, const float* s0, const void* dout, const float* ds,
+    const int32_t* lengths, void* dq, void* dk, void* dv, float* ds0, void* ws, size_t ws_bytes,
+    int32_t* status_dev, const pararnn_options_t* opts, void* stream) {
+  if (!la_sizes_ok(d)) return PARARNN_ERR_INVALID_ARGUMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d->B > 0 && d->L > 0) {
+    if (!q || !k || !v || !dout || !dq || !dk || !dv || !log_decay)
+      return PARARNN_ERR_INVALID_ARGUMENT;
+    if (!la_strides_ok(d->q_stride) || !la_strides_ok(d->k_stride) ||
+        !la_strides_ok(d->v_stride) || !la_strides_ok(d->do_stride))
+      return PARARNN_ERR_INVALID_ARGUMENT;
+    const void* ps[] = {q, k, v, dout, dq, dk, dv};
+    for (const void* x : ps)
+      if (!la_aligned(x, 16)) return PARARNN_ERR_INVALID_ARGUMENT;
+    if (!la_aligned(log_decay, 4) || !la_aligned(lengths, 4)) return PARARNN_ERR_INVALID_ARGUMENT;
+  }
+  if (!la_aligned(s0, 16) || !la_aligned(ds, 16) || !la_aligned(ds0, 16) || (ds && ds == ds0))
+    return PARARNN_ERR_INVALID_ARGUMENT;
+  const LaWs w = la_ws(d, true);
+  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
+  (void)opts;
+  if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
+    return PARARNN_ERR_CUDA;
+  if (d->B == 0) return PARARNN_OK;
+  if (d->L == 0)
+    return la_copy_state(ds, ds0, (size_t)d->B * d->H * d->Dk * d->Dv, st);
+
+  unsigned char* wb = static_cast<unsigned char*>(ws);
+  LaParams lp = {};
+  lp.npass = 3;
+  lp.log_decay = log_decay;
+  lp.lengths = lengths;
+  lp.B = (int)d->B;
+  lp.H = d->H;
+  lp.L = d->L;
+  lp.zero_tail = 1;
+  const LaIn iq = la_in(q, d->q_stride, d->H, d->Hq), ik = la_in(k, d->k_stride, d->H, d->Hk),
+             iv = la_in(v, d->v_stride, d->H, d->Hv),
+             io = la_in(dout, d->do_stride, d->H, d->H);
+  const struct {
+    LaIn q, k, v;
+    void* out;
+    size_t off;
+    int Hx, dk, dv, rev;
+    const float* s_in;
+  } def[3] = {
+      {io, iv, ik, dq, w.dq, d->Hq, d->Dv, d->Dk, 0, s0},   // dq
+      {iv, io, iq, dk, w.dk, d->Hk, d->Dv, d->Dk, 1, ds},   // dk
+      {ik, iq, io, dv, w.dv, d->Hv, d->Dk, d->Dv, 1, ds},   // dv
+  };
+  for (int i = 0; i < 3; ++i) {
+    LaPass& a = lp.pass[i];
+    a.q = def[i].q;
+    a.k = def[i].k;
+    a.v = def[i].v;
+    a.dk = def[i].dk;
+    a.dv = def[i].dv;
+    a.rev = def[i].rev;
+    a.o_f32 = def[i].Hx != d->H;
+    a.o = a.o_f32 ? (void*)(wb + def[i].off) : def[i].out;
+    a.oh = a.dv;
+    a.ot = (long long)d->H * a.dv;
+    a.ob = a.ot * d->L;
+    a.s_in = def[i].s_in;
+    a.s_out = i == 2 ? ds0 : nullptr;
+    // states are stored [Dk, Dv]; the dq and dk passes carry the transpose
+    a.s_r = i == 2 ? d->Dv : 1;
+    a.s_c = i == 2 ? 1 : d->Dv;
+    a.c_out = i == 0 ? d->scale : 1.0f;
+    a.c_kv = i == 0 ? 1.0f : d->scale;
+  }
+  pararnn_status_t rc = la_launch_recurrent(lp, true, st);
+  for (int i = 0; i < 3 && rc == PARARNN_OK; ++i)
+    if (lp.pass[i].o_f32)
+      rc = la_group(static_cast<const float*>(lp.pass[i].o), def[i].out, d, def[i].Hx,
+                    lp.pass[i].dv, st);
+  return rc;
+}
+
+extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, const void* q,
+                                                 const void* k, const void* v,
+                                                 pararnn_dtype_t dtype, const float* log_decay,
+                                                 const float* s_prev, void* o, float* s_next,
+                                                 void* stream) {
+  if (!la_sizes_ok(d) || d->L != 1) return PARARNN_ERR_INVALID_ARGUMENT;
+  if (dtype != PARARNN_F32 && dtype != PARARNN_BF16) return PARARNN_ERR_INVALID_ARGUMENT;
+  if (d->B == 0) return PARARNN_OK;
+  if (!q || !k || !v || !o || !log_decay || !s_next) return PARARNN_ERR_INVALID_ARGUMENT;
+  const size_t es = dtype == PARARNN_F32 ? 4 : 2;
+  if (!la_aligned(q, es) || !la_aligned(k, es) || !la_aligned(v, es) || !la_aligned(o, es) ||
+      !la_aligned(log_decay, 4) || !la_aligned(s_prev, 16) || !la_aligned(s_next, 16))
+    return PARARNN_ERR_INVALID_ARGUMENT;
+  LaParams lp = {};
+  lp.npass = 1;
+  lp.log_decay = log_decay;
+  lp.B = (int)d->B;
+  lp.H = d->H;
+  lp.L = 1;
+  LaPass& a = lp.pass[0];
+  a.q = la_in(q, d->q_stride, d->H, d->Hq);
+  a.k = la_in(k, d->k_stride, d->H, d->Hk);
+  a.v = la_in(v, d->v_stride, d->H, d->Hv);
+  a.o = o;
+  a.oh = d->Dv;
+  a.ot = 0;
+  a.ob = (long long)d->H * d->Dv;
+  a.s_in = s_prev;
+  a.s_out = s_next;
+  a.s_r = d->Dv;
+  a.s_c = 1;
+  a.dk = d->Dk;
+  a.dv = d->Dv;
+  a.o_f32 = dtype == PARARNN_F32;
+  a.c_out = d->scale;
+  a.c_kv = 1.0f;
+  return la_launch_recurrent(lp, dtype == PARARNN_BF16, static_cast<cudaStream_t>(stream));
+}

@@ -1,0 +1,229 @@
+// pararnn_linattn.cuh -- linear attention with one decay per head: the affine
+// scan whose state is a Dk x Dv matrix per (batch row, head).
+//
+//   S_t = gamma S_{t-1} + k_t^T v_t,   o_t = q_t S_t,   gamma = exp(log_decay[h])
+//
+// Every kernel here computes one "pass": a walk over time that reads three
+// streams (q, k, v roles), carries the state and writes one output stream.
+// The forward scan is one such pass; the gradients are three:
+//   dq = pass(q: do, k: v, v: k),  forwards, state S^T
+//   dk = pass(q: v, k: do, v: q),  backwards, state dS^T
+//   dv = pass(q: k, k: q, v: do),  backwards, state dS
+// Going backwards the carried state is D = dl/dS_{t-1}: at token t
+//   R = D + c_kv k_t^T v_t,  o_t = c_out q_t R,  D <- gamma R,
+// and going forwards
+//   S <- gamma S + c_kv k_t^T v_t,  o_t = c_out q_t S.
+// c_out and c_kv place the attention scale where it belongs in each pass.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace pararnn {
+
+constexpr int kLaMaxDim = 128;   // largest Dk and Dv
+constexpr int kLaMaxPasses = 3;
+
+// One input stream [B, L, Hx, D]: element strides, and the number of heads of
+// the pass that share one head of the stream.
+struct LaIn {
+  const void* p;
+  long long sb, st, sh;
+  int rep;
+};
+
+struct LaPass {
+  LaIn q, k, v;
+  void* o;               // [B, L, H, dv]: bf16, or fp32 where o_f32
+  long long ob, ot, oh;  // element strides of o
+  const float* s_in;     // initial state or NULL (= 0): element (r, c) of (b, h) at
+  float* s_out;          //   ((b H + h) dk dv) + r s_r + c s_c;  final state or NULL
+  long long s_r, s_c;    // the strides of s_in
+  int dk, dv;            // contraction and output sizes of this pass
+  int rev;               // 1: backwards in time
+  int o_f32;
+  float c_out, c_kv;
+};
+
+struct LaParams {
+  LaPass pass[kLaMaxPasses];
+  int npass;
+  const float* log_decay;  // [H]
+  const int* lengths;      // [B] or NULL (= L)
+  int B, H;
+  long long L;
+  int zero_tail;           // write zeros to output rows at and after the length
+};
+
+__device__ __forceinline__ float la_load(const float* p) { return *p; }
+__device__ __forceinline__ float la_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ long long la_length(const LaParams& p, int b) {
+  if (!p.lengths) return p.L;
+  const long long n = p.lengths[b];
+  return n < 0 ? 0 : (n > p.L ? p.L : n);
+}
+
+// ---------------------------------------------------------------------------
+// Recurrent form.  A CTA holds a 32-column tile of one (b, h) state in
+// registers (8 lanes x float4 across, 32 row groups down, at most 4 rows a
+// thread) and walks the tokens, kLaRecT at a time: the tokens' q, k and v are
+// staged in shared memory as fp32, every thread updates its rows and adds up
+// its part of q S, and the row groups' parts are joined once per batch of
+// tokens.  All arithmetic is fp32.  One token (the decode step) is the case
+// L = 1: it reads and writes the state once and is bound by that traffic.
+// ---------------------------------------------------------------------------
+constexpr int kLaRecT = 8;
+constexpr int kLaRecThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kLaRecThreads)
+    pararnn_linattn_recurrent_kernel(const __grid_constant__ LaParams p) {
+  __shared__ float s_q[kLaRecT][kLaMaxDim], s_k[kLaRecT][kLaMaxDim];
+  __shared__ __align__(16) float s_v[kLaRecT][32];
+  __shared__ float s_part[kLaRecT][8][32];
+
+  const LaPass& a = p.pass[blockIdx.z];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int c0 = blockIdx.y * 32;
+  if (c0 >= a.dv) return;
+  const int b = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
+  const int cg = lane & 7, rg = warp * 4 + (lane >> 3);
+  const int col = c0 + cg * 4;  // dv is a multiple of 8: a group of 4 is whole
+  const bool cok = col < a.dv;
+  const long long n = la_length(p, b);
+  // gamma as a sum of two floats: a slow head's memory multiplies by it thousands
+  // of times, and the half step that one float leaves (2^-25 near 1) would add up
+  // in the same direction every time
+  const double gd = exp((double)p.log_decay[h]);
+  const float gamma = (float)gd, glow = isfinite(gamma) ? (float)(gd - (double)gamma) : 0.0f;
+  const long long sbase = ((long long)b * p.H + h) * a.dk * a.dv;
+
+  float s[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = r * 32 + rg;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[r][c] = 0.0f;
+    if (a.s_in && cok && row < a.dk) {
+      const float* sp = a.s_in + sbase + row * a.s_r + col * a.s_c;
+      if (a.s_c == 1) {
+        const float4 x = *reinterpret_cast<const float4*>(sp);
+        s[r][0] = x.x, s[r][1] = x.y, s[r][2] = x.z, s[r][3] = x.w;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[r][c] = sp[c * a.s_c];
+      }
+    }
+  }
+
+  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
+  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
+  const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
+  const long long obase = b * a.ob + h * a.oh;
+
+  for (long long i0 = 0; i0 < n; i0 += kLaRecT) {
+    const int m = (int)(n - i0 < kLaRecT ? n - i0 : kLaRecT);
+    for (int e = tid; e < m * a.dk; e += kLaRecThreads) {
+      const int j = e / a.dk, d = e % a.dk;
+      const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
+      s_q[j][d] = la_load(q + t * a.q.st + d);
+      s_k[j][d] = la_load(k + t * a.k.st + d);
+    }
+    {
+      const int j = tid >> 5, d = c0 + lane;
+      const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
+      if (j < m) s_v[j][lane] = d < a.dv ? a.c_kv * la_load(v + t * a.v.st + d) : 0.0f;
+    }
+    __syncthreads();
+    for (int j = 0; j < m; ++j) {
+      const float4 vv = *reinterpret_cast<const float4*>(&s_v[j][cg * 4]);
+      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = r * 32 + rg;
+        if (row < a.dk) {
+          const float kk = s_k[j][row], qq = s_q[j][row];
+          const float x[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float old = s[r][c];
+            const float w = fmaf(kk, x[c], a.rev ? old : fmaf(gamma, old, glow * old));
+            o[c] = fmaf(qq, w, o[c]);
+            s[r][c] = a.rev ? fmaf(gamma, w, glow * w) : w;
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        o[c] += __shfl_xor_sync(0xffffffffu, o[c], 8);
+        o[c] += __shfl_xor_sync(0xffffffffu, o[c], 16);
+        if (lane < 8) s_part[j][warp][cg * 4 + c] = o[c];
+      }
+    }
+    __syncthreads();
+    {
+      const int j = tid >> 5, d = c0 + lane;
+      if (j < m && d < a.dv) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) x += s_part[j][w][lane];
+        x *= a.c_out;
+        const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
+        const long long at = obase + t * a.ot + d;
+        if (a.o_f32)
+          static_cast<float*>(a.o)[at] = x;
+        else
+          static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(x);
+      }
+    }
+    // the next batch's staging writes s_q/s_k/s_v, which no thread reads any
+    // more; s_part is rewritten only after the next barrier
+  }
+
+  if (a.s_out && cok) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = r * 32 + rg;
+      if (row < a.dk)
+        *reinterpret_cast<float4*>(a.s_out + sbase + (long long)row * a.dv + col) =
+            make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+    }
+  }
+  if (p.zero_tail) {
+    const int rows = kLaRecThreads / 32, d = c0 + lane;
+    for (long long t = n + warp; t < p.L; t += rows)
+      if (d < a.dv) {
+        const long long at = obase + t * a.ot + d;
+        if (a.o_f32)
+          static_cast<float*>(a.o)[at] = 0.0f;
+        else
+          static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(0.0f);
+      }
+  }
+}
+
+// Gradient of a stream whose heads are shared: the fp32 gradients of the H
+// heads [rows, H, D] summed in head order over each group -> bf16 [rows, Hx, D].
+__global__ void pararnn_linattn_group_kernel(const float* x, __nv_bfloat16* y, long long rows,
+                                             int H, int Hx, int D) {
+  const int rep = H / Hx, D4 = D / 4;
+  const long long n = rows * Hx * D4;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
+       i += (long long)gridDim.x * blockDim.x) {
+    const long long rh = i / D4;  // row * Hx + hx
+    const int d = (int)(i % D4) * 4;
+    const float* s = x + (rh * rep) * D + d;
+    float4 acc = *reinterpret_cast<const float4*>(s);
+    for (int g = 1; g < rep; ++g) {
+      const float4 w = *reinterpret_cast<const float4*>(s + (long long)g * D);
+      acc.x += w.x, acc.y += w.y, acc.z += w.z, acc.w += w.w;
+    }
+    __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(y + rh * D + d);
+    out[0] = __floats2bfloat162_rn(acc.x, acc.y);
+    out[1] = __floats2bfloat162_rn(acc.z, acc.w);
+  }
+}
+
+}  // namespace pararnn
