@@ -68,11 +68,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         jobs.append((cmd, obj, subprocess.Popen(cmd)))
-    failed = [(cmd, rc) for cmd, _, job in jobs if (rc := job.wait()) != 0]
+    failed = None
+    for cmd, obj, job in jobs:
+        rc = job.wait()
+        if rc == 0:
+            os.replace(obj + ".tmp", obj)
+        else:
+            failed = failed or subprocess.CalledProcessError(rc, cmd)
     if failed:
-        raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
-    for _, obj, _ in jobs:
-        os.replace(obj + ".tmp", obj)
+        raise failed
     subprocess.check_call([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
                            *[_object(s) for s in SOURCES], "-o", LIB + ".tmp"])
     os.replace(LIB + ".tmp", LIB)

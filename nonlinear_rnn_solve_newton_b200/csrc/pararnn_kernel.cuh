@@ -514,7 +514,7 @@ __device__ __forceinline__ int sweep_stops(const unsigned* rho_bits, int k0, int
 // release.  Bounded; returns false if the kernel is aborting or the wait ran
 // out.  The signature stays one small struct: the callers' hot loops compile as
 // if the call were not there.
-__device__ __noinline__ bool grid_barrier(WaitCtx p) {
+__device__ __noinline__ inline bool grid_barrier(WaitCtx p) {
   __shared__ int s_ok;
   __threadfence();  // every thread: its iterate and residuals before the CTA arrives
   __syncthreads();
@@ -552,7 +552,7 @@ __device__ __noinline__ bool grid_barrier(WaitCtx p) {
 // (the first iterate within tol, or the first non-finite residual, else the
 // last evaluated), convergence and status.  `extra_status` replaces a zero
 // status (e.g. a wait that ran out in this thread's own CTA).
-__device__ __noinline__ void write_solve_info(void* info_ptr, Ctrl* ctrl,
+__device__ __noinline__ inline void write_solve_info(void* info_ptr, Ctrl* ctrl,
                                                  const unsigned* rho_bits, int last, int passes,
                                                  int max_iters, float tol, unsigned extra_status) {
   struct Info {

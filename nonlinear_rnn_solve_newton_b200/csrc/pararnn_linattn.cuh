@@ -54,6 +54,8 @@ struct LaParams {
   int B, H;
   long long L;
   int zero_tail;           // write zeros to output rows at and after the length
+  int* status_dev;         // 0 / 4, or NULL
+  long long timeout_ns;    // bound of the chunked form's waits
 };
 
 __device__ __forceinline__ float la_load(const float* p) { return *p; }

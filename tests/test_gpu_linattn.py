@@ -103,17 +103,24 @@ SHAPES = [(1, 1, 1, 1, 1, 1, 8, 8), (2, 2, 3, 3, 3, 3, 64, 64), (3, 15, 2, 2, 2,
           (1, 777, 2, 2, 2, 2, 120, 8), (1, 1025, 1, 1, 1, 1, 128, 128)]
 
 
+FORMS = {"auto": 0, "recurrent": 1, "chunks": 2}
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("shape", SHAPES)
-def test_scan(pr, shape):
+def test_scan(pr, shape, form):
     x, _ = make(*shape, seed=1)
-    check_scan(pr, x, 0.3, pr.scan_linattn(**on_gpu(x), scale=0.3))
+    got = pr.scan_linattn(**on_gpu(x), scale=0.3, opts=pr.Options(regime=FORMS[form]))
+    check_scan(pr, x, 0.3, got)
 
 
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("shape", SHAPES)
-def test_backward(pr, shape):
+def test_backward(pr, shape, form):
     x, y = make(*shape, seed=2)
     g = on_gpu(x)
-    got = pr.scan_linattn_backward(**g, do=dev(y["do"], BF), ds=dev(y["ds"]), scale=0.3)
+    got = pr.scan_linattn_backward(**g, do=dev(y["do"], BF), ds=dev(y["ds"]), scale=0.3,
+                                   opts=pr.Options(regime=FORMS[form]))
     check_backward(pr, x, y, 0.3, got)
 
 
