@@ -72,10 +72,11 @@ PFN_cuTensorMapEncodeTiled_v12000 la_encoder() {
 
 // A stream [B, L, Hx, D] as a 4-D tensor {D, L, Hx, B}: boxes of 64 columns (one
 // 128-byte swizzle row) x 128 tokens of one head; what lies outside reads as zero.
-bool la_map(CUtensorMap* m, const LaIn& in, int D, int Hx, const LaParams& lp) {
+bool la_map(CUtensorMap* m, const LaIn& in, int D, const LaParams& lp) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = la_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)lp.L, (cuuint64_t)Hx, (cuuint64_t)lp.B};
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)lp.L, (cuuint64_t)(lp.H / in.rep),
+                              (cuuint64_t)lp.B};
   const cuuint64_t strides[3] = {(cuuint64_t)in.st * 2, (cuuint64_t)in.sh * 2,
                                  (cuuint64_t)in.sb * 2};
   const cuuint32_t box[4] = {64, kLaT, 1, 1};
@@ -86,11 +87,9 @@ bool la_map(CUtensorMap* m, const LaIn& in, int D, int Hx, const LaParams& lp) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KD>
+template <int KD, bool FULL>
 pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStream_t st) {
-  int dv = 0;
-  for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
-  const void* fn = (const void*)pararnn_linattn_chunk_kernel<KD>;
+  const void* fn = (const void*)pararnn_linattn_chunk_kernel<KD, FULL>;
   const size_t smem = LaSmem<KD>::kBytes;
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) {
@@ -102,40 +101,88 @@ pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStrea
     cudaGetLastError();
     return PARARNN_ERR_CUDA;
   }
-  const dim3 grid((unsigned)((long long)lp.B * lp.H), (unsigned)((dv + kLaN - 1) / kLaN),
-                  (unsigned)lp.npass);
-  pararnn_linattn_chunk_kernel<KD><<<grid, kLaThreads, smem, st>>>(lp, tm);
+  int dv = 0;
+  for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
+  const dim3 grid((unsigned)((long long)lp.B * lp.H * lp.nspan),
+                  (unsigned)((dv + kLaN - 1) / kLaN), (unsigned)lp.npass);
+  pararnn_linattn_chunk_kernel<KD, FULL><<<grid, kLaThreads, smem, st>>>(lp, tm);
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }
 
-// The form of a call.  The recurrent form takes about a microsecond per 8 tokens
-// whatever the batch, the chunked one a few microseconds per 128.
+// The form of a call and, for the chunked form, the spans that time is cut into.
+// The recurrent form takes about a microsecond per 8 tokens whatever the batch, the
+// chunked one a few microseconds per 128.
 constexpr long long kLaRecurrentMax = 16;
+constexpr long long kLaSms = 148;  // one CTA of the chunked form each
 
-pararnn_status_t la_launch(LaParams& lp, const pararnn_options_t* opts, int32_t* status_dev,
-                           cudaStream_t st) {
+struct LaPlan {
+  bool recurrent;
+  int nspan;
+  long long span;  // tokens
+};
+
+LaPlan la_plan(const pararnn_linattn_t* d, bool backward, const pararnn_options_t* opts) {
   const int form = opts ? opts->regime : 0;
-  if (form == 1 || (form == 0 && lp.L <= kLaRecurrentMax)) return la_launch_recurrent(lp, true, st);
+  LaPlan pl = {form == 1 || (form == 0 && d->L <= kLaRecurrentMax), 1, d->L};
+  if (pl.recurrent) return pl;
+  const long long tk = (d->Dk + kLaN - 1) / kLaN, tv = (d->Dv + kLaN - 1) / kLaN;
+  const long long items = d->B * d->H * (backward ? 2 * tk + tv : tv);
+  const long long chunks = (d->L + kLaT - 1) / kLaT;
+  if (items >= 4 * kLaSms) return pl;
+  // in units of one chunk's walk: a CTA costs about two to start; with more than one
+  // span the states are walked first (two thirds of the work) and two more kernels start
+  double best = 0.0;
+  for (long long want = 1; want <= chunks && want <= kLaSms; ++want) {
+    const long long len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
+    const long long waves = (items * n + kLaSms - 1) / kLaSms;
+    const double cost = n > 1 ? waves * (1.67 * len + 4.0) + 6.0 : waves * (len + 2.0);
+    if (want == 1 || cost < best) {
+      best = cost;
+      pl.nspan = (int)n;
+      pl.span = n > 1 ? len * kLaT : d->L;
+    }
+  }
+  return pl;
+}
+
+pararnn_status_t la_launch(LaParams& lp, const LaPlan& pl, float* span_ws,
+                           const pararnn_options_t* opts, int32_t* status_dev, cudaStream_t st) {
+  lp.nspan = pl.nspan;
+  lp.span = pl.span;
+  if (pl.recurrent) return la_launch_recurrent(lp, true, st);
+  if (pl.nspan > 1)
+    for (int i = 0; i < lp.npass; ++i) {
+      lp.pass[i].s_span = span_ws;
+      span_ws += (size_t)lp.B * lp.H * pl.nspan * lp.pass[i].dk * lp.pass[i].dv;
+    }
   lp.status_dev = status_dev;
   lp.timeout_ns = opts && opts->wait_timeout_ns > 0 ? opts->wait_timeout_ns : 1000000000LL;
-  LaMaps tm;
+  LaMaps tm = {};
   int dk = 0;
   for (int i = 0; i < lp.npass; ++i) {
     const LaPass& a = lp.pass[i];
-    if (!la_map(&tm.q[i], a.q, a.dk, lp.H / a.q.rep, lp) ||
-        !la_map(&tm.k[i], a.k, a.dk, lp.H / a.k.rep, lp) ||
-        !la_map(&tm.v[i], a.v, a.dv, lp.H / a.v.rep, lp))
+    if (!la_map(&tm.q[i], a.q, a.dk, lp) || !la_map(&tm.k[i], a.k, a.dk, lp) ||
+        !la_map(&tm.v[i], a.v, a.dv, lp))
       return PARARNN_ERR_INVALID_ARGUMENT;
     dk = a.dk > dk ? a.dk : dk;
   }
-  return dk <= 64 ? la_launch_chunk<64>(lp, tm, st) : la_launch_chunk<128>(lp, tm, st);
+  pararnn_status_t rc = PARARNN_OK;
+  if (lp.nspan > 1) {
+    rc = dk <= 64 ? la_launch_chunk<64, false>(lp, tm, st) : la_launch_chunk<128, false>(lp, tm, st);
+    if (rc != PARARNN_OK) return rc;
+    pararnn_linattn_join_kernel<<<dim3((unsigned)((long long)lp.B * lp.H), 8, (unsigned)lp.npass),
+                                  256, 0, st>>>(lp);
+    if (cudaGetLastError() != cudaSuccess) return PARARNN_ERR_CUDA;
+  }
+  return dk <= 64 ? la_launch_chunk<64, true>(lp, tm, st) : la_launch_chunk<128, true>(lp, tm, st);
 }
 
-// Workspace: fp32 per-head gradients of the streams whose heads are shared.
+// Workspace: fp32 per-head gradients of the streams whose heads are shared, and
+// the spans' states of every pass.
 struct LaWs {
-  size_t dq, dk, dv, total;
+  size_t dq, dk, dv, span, total;
 };
-LaWs la_ws(const pararnn_linattn_t* d, bool backward) {
+LaWs la_ws(const pararnn_linattn_t* d, bool backward, const LaPlan& pl) {
   LaWs w = {};
   size_t at = 0;
   const size_t rows = (size_t)d->B * (size_t)d->L * (size_t)d->H;
@@ -147,6 +194,9 @@ LaWs la_ws(const pararnn_linattn_t* d, bool backward) {
     w.dv = at;
     if (d->Hv != d->H) at += la_round(rows * d->Dv * 4);
   }
+  w.span = at;
+  if (pl.nspan > 1)
+    at += la_round((size_t)(backward ? 3 : 1) * d->B * d->H * pl.nspan * d->Dk * d->Dv * 4);
   w.total = at ? at : 256;
   return w;
 }
@@ -177,7 +227,7 @@ using namespace pararnn;
 
 extern "C" size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* d, int32_t backward) {
   if (!la_sizes_ok(d)) return 0;
-  return la_ws(d, backward != 0).total;
+  return la_ws(d, backward != 0, la_plan(d, backward != 0, nullptr)).total;
 }
 
 extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, const void* q,
@@ -197,9 +247,10 @@ extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, con
       return PARARNN_ERR_INVALID_ARGUMENT;
   }
   if (!la_aligned(s0, 16) || !la_aligned(s, 16)) return PARARNN_ERR_INVALID_ARGUMENT;
-  const LaWs w = la_ws(d, false);
-  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
+  const LaPlan pl = la_plan(d, false, opts);
+  const LaWs w = la_ws(d, false, pl);
+  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
   if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
     return PARARNN_ERR_CUDA;
   if (d->B == 0) return PARARNN_OK;
@@ -229,7 +280,7 @@ extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, con
   a.dv = d->Dv;
   a.c_out = d->scale;
   a.c_kv = 1.0f;
-  return la_launch(lp, opts, status_dev, st);
+  return la_launch(lp, pl, static_cast<float*>(ws), opts, status_dev, st);
 }
 
 extern "C" pararnn_status_t pararnn_scan_linattn_backward(
@@ -252,9 +303,10 @@ extern "C" pararnn_status_t pararnn_scan_linattn_backward(
   }
   if (!la_aligned(s0, 16) || !la_aligned(ds, 16) || !la_aligned(ds0, 16) || (ds && ds == ds0))
     return PARARNN_ERR_INVALID_ARGUMENT;
-  const LaWs w = la_ws(d, true);
-  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
+  const LaPlan pl = la_plan(d, true, opts);
+  const LaWs w = la_ws(d, true, pl);
+  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
   if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
     return PARARNN_ERR_CUDA;
   if (d->B == 0) return PARARNN_OK;
@@ -305,7 +357,8 @@ extern "C" pararnn_status_t pararnn_scan_linattn_backward(
     a.c_out = i == 0 ? d->scale : 1.0f;
     a.c_kv = i == 0 ? 1.0f : d->scale;
   }
-  pararnn_status_t rc = la_launch(lp, opts, status_dev, st);
+  pararnn_status_t rc =
+      la_launch(lp, pl, reinterpret_cast<float*>(wb + w.span), opts, status_dev, st);
   for (int i = 0; i < 3 && rc == PARARNN_OK; ++i)
     if (lp.pass[i].o_f32)
       rc = la_group(static_cast<const float*>(lp.pass[i].o), def[i].out, d, def[i].Hx,
@@ -332,6 +385,8 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   lp.B = (int)d->B;
   lp.H = d->H;
   lp.L = 1;
+  lp.nspan = 1;
+  lp.span = 1;
   LaPass& a = lp.pass[0];
   a.q = la_in(q, d->q_stride, d->H, d->Hq);
   a.k = la_in(k, d->k_stride, d->H, d->Hk);

@@ -40,6 +40,7 @@ struct LaPass {
   const float* s_in;     // initial state or NULL (= 0): element (r, c) of (b, h) at
   float* s_out;          //   ((b H + h) dk dv) + r s_r + c s_c;  final state or NULL
   long long s_r, s_c;    // the strides of s_in
+  float* s_span;         // the spans' states, [B, H, spans, dk, dv]
   int dk, dv;            // contraction and output sizes of this pass
   int rev;               // 1: backwards in time
   int o_f32;
@@ -56,6 +57,8 @@ struct LaParams {
   int zero_tail;           // write zeros to output rows at and after the length
   int* status_dev;         // 0 / 4, or NULL
   long long timeout_ns;    // bound of the chunked form's waits
+  int nspan;               // spans of time, walked side by side
+  long long span;          // tokens of a span
 };
 
 __device__ __forceinline__ float la_load(const float* p) { return *p; }
@@ -67,55 +70,79 @@ __device__ __forceinline__ long long la_length(const LaParams& p, int b) {
   return n < 0 ? 0 : (n > p.L ? p.L : n);
 }
 
+// Tokens of span g of batch row b (one span: the whole row).
+__device__ __forceinline__ long long la_span_tokens(const LaParams& p, int b, int g) {
+  const long long n = la_length(p, b) - g * p.span;
+  return n < 0 ? 0 : (p.nspan > 1 && n > p.span ? p.span : n);
+}
+
+// x = hi + lo with hi the nearest float (0 beyond the range of a float)
+__device__ __forceinline__ void la_two(double x, float& hi, float& lo) {
+  hi = (float)x;
+  lo = isfinite(hi) ? (float)(x - (double)hi) : 0.0f;
+}
+
+// gamma^i in 64 bits; gamma^0 = 1 also for gamma = 0
+__device__ __forceinline__ double la_powl(float log_decay, long long i) {
+  return i == 0 ? 1.0 : exp((double)log_decay * (double)i);
+}
+__device__ __forceinline__ double la_pow(float log_decay, int i) { return la_powl(log_decay, i); }
+
 // ---------------------------------------------------------------------------
-// Recurrent form.  A CTA holds a 32-column tile of one (b, h) state in
-// registers (8 lanes x float4 across, 32 row groups down, at most 4 rows a
-// thread) and walks the tokens, kLaRecT at a time: the tokens' q, k and v are
-// staged in shared memory as fp32, every thread updates its rows and adds up
-// its part of q S, and the row groups' parts are joined once per batch of
-// tokens.  All arithmetic is fp32.  One token (the decode step) is the case
-// L = 1: it reads and writes the state once and is bound by that traffic.
+// Recurrent form.  THREADS threads hold a COLS-column tile of one (b, h) state in
+// registers (float4 across, the rest row groups, at most 4 rows a thread) and
+// walk the tokens, kLaRecT at a time: the tokens' q, k and v are staged in shared
+// memory as fp32, every thread updates its rows and adds up its part of q S, and
+// the row groups' parts are joined once per batch of tokens.  All arithmetic is
+// fp32.  One token (the decode step) is the case L = 1: it reads and writes the
+// state once and is bound by that traffic.
 // ---------------------------------------------------------------------------
 constexpr int kLaRecT = 8;
+constexpr int kLaRecCols = 32;
 constexpr int kLaRecThreads = 256;
 
-template <typename T>
-__global__ void __launch_bounds__(kLaRecThreads)
-    pararnn_linattn_recurrent_kernel(const __grid_constant__ LaParams p) {
-  __shared__ float s_q[kLaRecT][kLaMaxDim], s_k[kLaRecT][kLaMaxDim];
-  __shared__ __align__(16) float s_v[kLaRecT][32];
-  __shared__ float s_part[kLaRecT][8][32];
+template <int COLS> struct LaWalkSmem {
+  float q[kLaRecT][kLaMaxDim], k[kLaRecT][kLaMaxDim];
+  float v[kLaRecT][COLS];
+  float part[kLaRecT][16][COLS];  // one row per warp
+};
 
-  const LaPass& a = p.pass[blockIdx.z];
+// Tokens [tb, tb + n) of (b, h), columns c0 .. c0 + COLS - 1, state at element
+// (r, c) of s_in + r sr + c sc (NULL = 0); the state behind them to s_out (dense).
+template <typename T, int COLS, int THREADS>
+__device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, int h, int c0,
+                                     long long tb, long long n, const float* s_in, long long sr,
+                                     long long sc, float* s_out, LaWalkSmem<COLS>& sm) {
+  constexpr int CG = COLS / 4;          // threads across
+  constexpr int RG = THREADS / CG;      // row groups: rows rg, rg + RG, ...
+  constexpr int R = kLaMaxDim / RG;     // rows a thread
+  constexpr int NW = THREADS / 32;
+  static_assert(R * RG == kLaMaxDim && NW <= 16 && CG <= 16, "tile");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int c0 = blockIdx.y * 32;
-  if (c0 >= a.dv) return;
-  const int b = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
-  const int cg = lane & 7, rg = warp * 4 + (lane >> 3);
+  const int cg = tid % CG, rg = tid / CG;
   const int col = c0 + cg * 4;  // dv is a multiple of 8: a group of 4 is whole
   const bool cok = col < a.dv;
-  const long long n = la_length(p, b);
+  const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
   // gamma as a sum of two floats: a slow head's memory multiplies by it thousands
   // of times, and the half step that one float leaves (2^-25 near 1) would add up
   // in the same direction every time
-  const double gd = exp((double)p.log_decay[h]);
-  const float gamma = (float)gd, glow = isfinite(gamma) ? (float)(gd - (double)gamma) : 0.0f;
-  const long long sbase = ((long long)b * p.H + h) * a.dk * a.dv;
+  float gamma, glow;
+  la_two(exp((double)p.log_decay[h]), gamma, glow);
 
-  float s[4][4];
+  float s[R][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = r * 32 + rg;
+  for (int r = 0; r < R; ++r) {
+    const int row = r * RG + rg;
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[r][c] = 0.0f;
-    if (a.s_in && cok && row < a.dk) {
-      const float* sp = a.s_in + sbase + row * a.s_r + col * a.s_c;
-      if (a.s_c == 1) {
+    if (s_in && cok && row < a.dk) {
+      const float* sp = s_in + row * sr + col * sc;
+      if (sc == 1) {
         const float4 x = *reinterpret_cast<const float4*>(sp);
         s[r][0] = x.x, s[r][1] = x.y, s[r][2] = x.z, s[r][3] = x.w;
       } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] = sp[c * a.s_c];
+        for (int c = 0; c < 4; ++c) s[r][c] = sp[c * sc];
       }
     }
   }
@@ -124,30 +151,34 @@ __global__ void __launch_bounds__(kLaRecThreads)
   const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
   const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
   const long long obase = b * a.ob + h * a.oh;
+  const long long first = a.rev ? tb + n - 1 : tb;
+  const int dir = a.rev ? -1 : 1;
 
   for (long long i0 = 0; i0 < n; i0 += kLaRecT) {
     const int m = (int)(n - i0 < kLaRecT ? n - i0 : kLaRecT);
-    for (int e = tid; e < m * a.dk; e += kLaRecThreads) {
+    sync();  // the staged tokens and parts of the batch before have been read
+    for (int e = tid; e < m * a.dk; e += THREADS) {
       const int j = e / a.dk, d = e % a.dk;
-      const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
-      s_q[j][d] = la_load(q + t * a.q.st + d);
-      s_k[j][d] = la_load(k + t * a.k.st + d);
+      const long long t = first + dir * (i0 + j);
+      sm.q[j][d] = la_load(q + t * a.q.st + d);
+      sm.k[j][d] = la_load(k + t * a.k.st + d);
     }
-    {
-      const int j = tid >> 5, d = c0 + lane;
-      const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
-      if (j < m) s_v[j][lane] = d < a.dv ? a.c_kv * la_load(v + t * a.v.st + d) : 0.0f;
+    for (int e = tid; e < m * COLS; e += THREADS) {
+      const int j = e / COLS, d = e % COLS;
+      const long long t = first + dir * (i0 + j);
+      sm.v[j][d] = c0 + d < a.dv ? a.c_kv * la_load(v + t * a.v.st + c0 + d) : 0.0f;
     }
-    __syncthreads();
+    sync();
     for (int j = 0; j < m; ++j) {
-      const float4 vv = *reinterpret_cast<const float4*>(&s_v[j][cg * 4]);
       float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float x[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = r * 32 + rg;
+      for (int c = 0; c < 4; ++c) x[c] = sm.v[j][cg * 4 + c];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int row = r * RG + rg;
         if (row < a.dk) {
-          const float kk = s_k[j][row], qq = s_q[j][row];
-          const float x[4] = {vv.x, vv.y, vv.z, vv.w};
+          const float kk = sm.k[j][row], qq = sm.q[j][row];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float old = s[r][c];
@@ -159,45 +190,56 @@ __global__ void __launch_bounds__(kLaRecThreads)
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        o[c] += __shfl_xor_sync(0xffffffffu, o[c], 8);
-        o[c] += __shfl_xor_sync(0xffffffffu, o[c], 16);
-        if (lane < 8) s_part[j][warp][cg * 4 + c] = o[c];
+#pragma unroll
+        for (int g = CG; g < 32; g <<= 1) o[c] += __shfl_xor_sync(0xffffffffu, o[c], g);
+        if (lane < CG) sm.part[j][warp][cg * 4 + c] = o[c];
       }
     }
-    __syncthreads();
-    {
-      const int j = tid >> 5, d = c0 + lane;
-      if (j < m && d < a.dv) {
+    sync();
+    for (int e = tid; e < m * COLS; e += THREADS) {
+      const int j = e / COLS, d = e % COLS;
+      if (c0 + d < a.dv) {
         float x = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) x += s_part[j][w][lane];
+        for (int w = 0; w < NW; ++w) x += sm.part[j][w][d];
         x *= a.c_out;
-        const long long t = a.rev ? n - 1 - (i0 + j) : i0 + j;
-        const long long at = obase + t * a.ot + d;
+        const long long at = obase + (first + dir * (i0 + j)) * a.ot + c0 + d;
         if (a.o_f32)
           static_cast<float*>(a.o)[at] = x;
         else
           static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(x);
       }
     }
-    // the next batch's staging writes s_q/s_k/s_v, which no thread reads any
-    // more; s_part is rewritten only after the next barrier
   }
 
-  if (a.s_out && cok) {
+  if (s_out && cok) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = r * 32 + rg;
+    for (int r = 0; r < R; ++r) {
+      const int row = r * RG + rg;
       if (row < a.dk)
-        *reinterpret_cast<float4*>(a.s_out + sbase + (long long)row * a.dv + col) =
+        *reinterpret_cast<float4*>(s_out + (long long)row * a.dv + col) =
             make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
     }
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLaRecThreads)
+    pararnn_linattn_recurrent_kernel(const __grid_constant__ LaParams p) {
+  __shared__ LaWalkSmem<kLaRecCols> sm;
+  const LaPass& a = p.pass[blockIdx.z];
+  const int c0 = blockIdx.y * kLaRecCols;
+  if (c0 >= a.dv) return;
+  const int b = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
+  const long long n = la_length(p, b);
+  const long long sb = ((long long)b * p.H + h) * a.dk * a.dv;
+  la_walk<T, kLaRecCols, kLaRecThreads>(p, a, b, h, c0, 0, n, a.s_in ? a.s_in + sb : nullptr, a.s_r,
+                                        a.s_c, a.s_out ? a.s_out + sb : nullptr, sm);
   if (p.zero_tail) {
-    const int rows = kLaRecThreads / 32, d = c0 + lane;
-    for (long long t = n + warp; t < p.L; t += rows)
+    const int warp = threadIdx.x >> 5, d = c0 + (threadIdx.x & 31);
+    for (long long t = n + warp; t < p.L; t += kLaRecThreads / 32)
       if (d < a.dv) {
-        const long long at = obase + t * a.ot + d;
+        const long long at = b * a.ob + h * a.oh + t * a.ot + d;
         if (a.o_f32)
           static_cast<float*>(a.o)[at] = 0.0f;
         else

@@ -8,9 +8,9 @@
 //   o_i  = c_out (gamma^(n-1-i) q_i D + c_kv sum_{j>=i} gamma^(j-i) (q_i.k_j) v_j)
 //   D'   = gamma^n D + sum_j k_j^T (c_kv gamma^(j+1) v_j)
 //
-// One CTA walks the chunks of one (batch row, head) and one 64-column tile of
-// the state, which stays in registers (fp32, one state row a thread).  Per chunk
-// four products run on the tensor cores:
+// One CTA walks the chunks of one (batch row, head), one span of time and one
+// 64-column tile of the state, which stays in registers (fp32, half a state row a
+// thread).  Per chunk four products run on the tensor cores:
 //   scores  S_qk = Q K^T           128 x 128 x dk    both operands K-major
 //   update  U    = K^T [V1 V2 V3]  dk x 192 x 128    both operands MN-major
 //   carried O_i  = Q S             128 x 64 x dk
@@ -22,8 +22,27 @@
 // an output that is itself rounded to bf16.
 //
 // Roles: warp 0 tensor copies (q, k, v of a chunk, two stages), warp 1 issues
-// the products, warps 2-5 weight the scores and write the outputs, warps 6-9
-// weight v, carry the state and write its bf16 copy.  Every wait is bounded.
+// the products, warps 2-9 weight the scores and write the outputs, warps 10-17
+// carry the state, weight v and write the state's bf16 copy.  Two warps share a
+// TMEM lane quarter and split its columns: with four warps a role, each
+// instruction was fetched for a single warp of an SM quarter and a third of the
+// issue slots waited for instructions.  The scores of the next chunk are made
+// before the local output of this one, so that weighting them (the longest step
+// outside the tensor cores) is off the path.  Every wait is bounded.
+//
+// TMEM (512 columns): two buffers of 128 for the scores -- the weighted scores
+// replace the lower half of a buffer, the local output then takes the upper --
+// 192 for the update, 64 for the carried output.
+//
+// A mask that multiplies by zero lets a non-finite k or v of a later token
+// of the chunk into an output.  Such a token also leaves the state non-finite
+// for good, so the end of the walk shows it: the CTA then walks its tokens
+// again with the recurrent form, which reads no token before its time.
+//
+// Spans: where (batch row, head, tile) give fewer CTAs than SMs, time is cut into
+// spans.  A first launch (FULL = false) computes the state that each span's own
+// tokens leave, pararnn_linattn_join_kernel carries them over the spans, and the
+// walk starts each span from the state before it.
 #pragma once
 
 #include "pararnn_linattn.cuh"
@@ -33,7 +52,8 @@ namespace pararnn {
 
 constexpr int kLaT = 128;  // tokens per chunk
 constexpr int kLaN = 64;   // state columns per CTA
-constexpr int kLaThreads = 320;
+constexpr int kLaThreads = 576;
+constexpr int kLaAgainThreads = 512;  // of the recurrent walk over non-finite inputs
 constexpr unsigned kLaBlk = kLaT * 128;  // a 128-row block of 64 bf16 columns
 
 template <int KD> struct LaSmem {
@@ -50,6 +70,29 @@ struct LaMaps {
   CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses];
 };
 
+// stage_wait with a thread that sleeps in the hardware for up to 2 us a try, so
+// that the waiting warps leave the issue slots to the working ones
+__device__ __forceinline__ bool la_try_wait(unsigned long long* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ bool la_wait(unsigned long long* bar, unsigned parity,
+                                        const WaitCtx& w) {
+  if (la_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (la_try_wait(bar, parity)) return true;
+    if (globaltimer() - t0 > (unsigned long long)w.timeout_ns) return false;
+  }
+}
+
 // MN-major operand written by tensor copies with the 128-byte swizzle: rows of
 // 64 elements along M or N, 8-row groups along K 1024 bytes apart (bits 32-45),
 // blocks of 64 along M or N kLaBlk apart (bits 16-29).
@@ -62,6 +105,18 @@ __device__ __forceinline__ unsigned long long umma_desc_mn_sw128(unsigned saddr)
 __host__ __device__ constexpr unsigned la_idesc(unsigned n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | (8u << 24);  // M = 128
+}
+
+// One thread of a converged warp.  The compiler keeps what such a thread uses in uniform
+// registers; under `lane == 0` it moves every descriptor there before each
+// tcgen05.mma.  Measured on B200, 8 MMAs of M = 128, N = 64 ... 192: 1400-1900
+// cycles to issue under lane == 0, 255-750 (the tensor pipe's own time) so.
+__device__ __forceinline__ bool la_elect() {
+  unsigned p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
 }
 
 // A from TMEM (lane = row, two bf16 of K per 32-bit column), B from shared memory.
@@ -86,17 +141,14 @@ __device__ __forceinline__ void tma_load_4d_s(unsigned dst, const CUtensorMap* m
       : "memory");
 }
 
-// 32 consecutive columns of this thread's TMEM lane, not waited for.
-__device__ __forceinline__ void tmem_ld32_async(unsigned taddr, unsigned* r) {
+// 16 consecutive columns of this thread's TMEM lane, not waited for.
+__device__ __forceinline__ void tmem_ld16_async(unsigned taddr, unsigned* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -118,6 +170,35 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const unsigned*>(&t);
 }
+// Two fp32 operations in one instruction, on a pair of neighbouring registers.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair2(float x, float y) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpair2(f32x2 d, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 pair2u(unsigned x, unsigned y) {
+  return pair2(__uint_as_float(x), __uint_as_float(y));
+}
+
 __device__ __forceinline__ float bf16_lo(unsigned u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(unsigned u) { return __uint_as_float(u & 0xFFFF0000u); }
 
@@ -137,53 +218,70 @@ __device__ __forceinline__ void sts128(unsigned a, unsigned x, unsigned y, unsig
                : "memory");
 }
 
-// x = hi + lo with hi the nearest float (0 beyond the range of a float)
-__device__ __forceinline__ void la_two(double x, float& hi, float& lo) {
-  hi = (float)x;
-  lo = isfinite(hi) ? (float)(x - (double)hi) : 0.0f;
+// 32 bytes to global memory: one store where the address is 32-byte aligned
+__device__ __forceinline__ void stg256(void* p, bool whole, const unsigned* w) {
+  if (whole)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
-// gamma^i in 64 bits; gamma^0 = 1 also for gamma = 0
-__device__ __forceinline__ double la_pow(float log_decay, int i) {
-  return i == 0 ? 1.0 : exp((double)log_decay * (double)i);
-}
-
-template <int KD>
+template <int KD, bool FULL>
 __global__ void __launch_bounds__(kLaThreads, 1)
     pararnn_linattn_chunk_kernel(const __grid_constant__ LaParams p,
                                  const __grid_constant__ LaMaps tm) {
   using Sm = LaSmem<KD>;
   extern __shared__ __align__(1024) unsigned char dsmem[];
-  __shared__ unsigned long long s_full[2], s_pv[2], s_sc, s_p, s_kv, s_qs, s_b, s_ofree, s_drain;
-  __shared__ __align__(16) float s_pw[kLaT + 4], s_col[32];
+  __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_sc[2], s_rd[4], s_p, s_kv, s_qs,
+      s_b, s_w, s_ofree, s_drain;
+  __shared__ float s_pw[kLaT + 1];        // gamma^i
+  // c_out c_kv gamma^d by distance d, in the order in which a row's columns need it:
+  // forwards d = 127 - x, backwards d = x - 32; 0 for the 32 distances below 0
+  __shared__ float s_wt[kLaT + 32];
   __shared__ unsigned s_tmem;
-  __shared__ int s_fail;
+  __shared__ int s_fail, s_bad;
 
   const LaPass& a = p.pass[blockIdx.z];
   const int col0 = blockIdx.y * kLaN;
   if (col0 >= a.dv) return;  // the whole CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
+  const int bh = (int)(blockIdx.x / p.nspan), span = (int)(blockIdx.x % p.nspan);
+  const int b = bh / p.H, h = bh % p.H;
   const unsigned sbase = (smem_u32(dsmem) + 1023u) & ~1023u;
   const WaitCtx wctx{nullptr, p.status_dev, p.timeout_ns};
-  const long long len = la_length(p, b);
+  // the tokens of this CTA: [tb, tb + len)
+  const long long tb = span * p.span;
+  const long long len = la_span_tokens(p, b, span);
   const int nc = (int)((len + kLaT - 1) / kLaT);
   const float ld = p.log_decay[h];
   const bool rev = a.rev != 0;
+  // the state before this span and behind it: element (r, c) at r s_r + c s_c
+  const long long sb = (p.nspan > 1 ? (long long)blockIdx.x : bh) * a.dk * a.dv;
+  const float* s_in = !FULL ? nullptr : p.nspan > 1 ? a.s_span : a.s_in;
+  float* s_out = !FULL ? a.s_span : p.nspan > 1 ? nullptr : a.s_out;
+  const long long sr = p.nspan > 1 ? a.dv : a.s_r, sc = p.nspan > 1 ? 1 : a.s_c;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
+      mbar_init(&s_vfull[s], 1);
       mbar_init(&s_pv[s], 1);
+      mbar_init(&s_sc[s], 1);
     }
-    mbar_init(&s_sc, 1);
+    for (int s = 0; s < 4; ++s) mbar_init(&s_rd[s], 32);
     mbar_init(&s_kv, 1);
     mbar_init(&s_qs, 1);
     mbar_init(&s_drain, 1);
-    mbar_init(&s_p, 128);
-    mbar_init(&s_b, 128);
-    mbar_init(&s_ofree, 128);
+    mbar_init(&s_p, 256);
+    mbar_init(&s_b, 256);
+    mbar_init(&s_w, 256);
+    mbar_init(&s_ofree, 256);
     s_fail = 0;
+    s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -194,19 +292,30 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (threadIdx.x >= 64 && threadIdx.x < 64 + kLaT + 1)
-    s_pw[threadIdx.x - 64] = (float)la_pow(ld, (int)threadIdx.x - 64);
-  if (threadIdx.x < 32)  // the column factor of a 32-column block off the diagonal
-    s_col[threadIdx.x] = (float)la_pow(ld, rev ? (int)threadIdx.x : 31 - (int)threadIdx.x);
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kLaT + 1) {
+    const int i = (int)threadIdx.x - 64;
+    const float g = (float)la_pow(ld, i);
+    s_pw[i] = g;
+    if (i < kLaT) s_wt[rev ? 32 + i : 127 - i] = a.c_out * a.c_kv * g;
+  } else if (threadIdx.x >= 256 && threadIdx.x < 288) {
+    s_wt[threadIdx.x - 256 + (rev ? 0 : kLaT)] = 0.0f;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const unsigned tmem = s_tmem;
-  const unsigned t_sc = tmem, t_p = tmem + 128, t_kv = tmem + 192, t_oi = tmem + 384,
-                 t_oa = tmem + 448;
+  const unsigned t_sc = tmem, t_kv = tmem + 256, t_oi = tmem + 448;
   // token of row 0 of the c-th chunk walked, and its number of tokens
-  const auto t0 = [&](int c) { return (rev ? nc - 1 - c : c) * kLaT; };
-  const auto rows = [&](int c) { return (int)(len - t0(c) < kLaT ? len - t0(c) : kLaT); };
+  const auto t0 = [&](int c) { return (int)tb + (rev ? nc - 1 - c : c) * kLaT; };
+  const auto rows = [&](int c) {
+    return (int)(tb + len - t0(c) < kLaT ? tb + len - t0(c) : kLaT);
+  };
+
+  // the state, and its bf16 copy's halves, belong to warps 10-17
+  const int qd = warp & 3, row = 32 * qd + lane, hf = warp < 10 ? (warp - 2) >> 2 : (warp - 10) >> 2;
+  const unsigned lane_off = (unsigned)(32 * qd) << 16;
+  f32x2 s[16];  // 32 columns of state row `row`, from column cs0
+  const int cs0 = col0 + 32 * hf;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -216,193 +325,234 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       int c = 0;
       for (; c < nc && !*(volatile int*)&s_fail; ++c) {
         const int st = c & 1;
-        // chunk c - 2 is done with this stage
-        if (c >= 2 && !stage_wait(&s_pv[st], (unsigned)((c >> 1) - 1) & 1u, wctx)) {
+        // the products of chunk c - 2 have read this stage
+        if (c >= 2 && !la_wait(&s_pv[st], (unsigned)((c >> 1) - 1) & 1u, wctx)) {
           s_fail = 1;
           break;
         }
-        mbar_expect_tx(&s_full[st], (2 * (KD / 64) + 1) * kLaBlk);
-        const int t = t0(c);
+        mbar_expect_tx(&s_full[st], (FULL ? 2 : 1) * (KD / 64) * kLaBlk);
 #pragma unroll
         for (int j = 0; j < KD / 64; ++j) {
           const unsigned off = (st * (KD / 64) + j) * kLaBlk;
-          tma_load_4d_s(sbase + Sm::kQ + off, mq, 64 * j, t, hq, b, &s_full[st]);
-          tma_load_4d_s(sbase + Sm::kK + off, mk, 64 * j, t, hk, b, &s_full[st]);
+          if (FULL) tma_load_4d_s(sbase + Sm::kQ + off, mq, 64 * j, t0(c), hq, b, &s_full[st]);
+          tma_load_4d_s(sbase + Sm::kK + off, mk, 64 * j, t0(c), hk, b, &s_full[st]);
         }
-        tma_load_4d_s(sbase + Sm::kV + st * kLaBlk, mv, col0, t, hv, b, &s_full[st]);
+        mbar_expect_tx(&s_vfull[st], kLaBlk);
+        tma_load_4d_s(sbase + Sm::kV + st * kLaBlk, mv, col0, t0(c), hv, b, &s_vfull[st]);
       }
       // no copy is in flight when the CTA exits (only a failed wait leaves one)
       WaitCtx last = wctx;
       if (last.timeout_ns < 2000000000LL) last.timeout_ns = 2000000000LL;
-      for (int i = c - 2 < 0 ? 0 : c - 2; i < c; ++i)
-        stage_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
+      for (int i = c - 2 < 0 ? 0 : c - 2; i < c; ++i) {
+        la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
+        la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
+      }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- products ---------------------------------------------------------------
-      for (int c = 0; c < nc && !*(volatile int*)&s_fail; ++c) {
-        const int st = c & 1;
-        const unsigned par = (unsigned)c & 1u;
-        const unsigned q = sbase + Sm::kQ + st * (KD / 64) * kLaBlk;
-        const unsigned k = sbase + Sm::kK + st * (KD / 64) * kLaBlk;
-        const unsigned v = sbase + Sm::kV + st * kLaBlk;
-        bool ok = stage_wait(&s_full[st], (unsigned)(c >> 1) & 1u, wctx);
-        if (ok) {
-          tc_fence_after();
+    // ---- products -----------------------------------------------------------------
+    // descriptors of stage 0; an address enters a descriptor in units of 16 bytes
+    const unsigned long long dq0 = umma_desc_sw128(sbase + Sm::kQ),
+                             dk0 = umma_desc_sw128(sbase + Sm::kK),
+                             dkt0 = umma_desc_mn_sw128(sbase + Sm::kK),
+                             dv0 = umma_desc_mn_sw128(sbase + Sm::kV),
+                             dw = umma_desc_mn_sw128(sbase + Sm::kVw),
+                             ds = umma_desc_mn_sw128(sbase + Sm::kS);
+    // the whole warp waits; true in every lane or in none
+    const auto wait = [&](unsigned long long* bar, unsigned parity) {
+      const bool ok = la_wait(bar, parity, wctx);
+      return __all_sync(0xffffffffu, ok) != 0;
+    };
+    const auto scores = [&](int c) {
+      const int st = c & 1;
+      if (!wait(&s_full[st], (unsigned)(c >> 1) & 1u)) return false;
+      tc_fence_after();
+      if (la_elect()) {
+        const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
 #pragma unroll
-          for (int i = 0; i < KD / 16; ++i) {
-            const unsigned off = (i >> 2) * kLaBlk + (i & 3) * 32u;
-            umma_f16_ss(t_sc, umma_desc_sw128(q + off), umma_desc_sw128(k + off),
-                        la_idesc(128, false, false), i != 0);
+        for (int i = 0; i < KD / 16; ++i) {
+          const unsigned off = stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u;
+          umma_f16_ss(t_sc + 128 * st, dq0 + off, dk0 + off, la_idesc(128, false, false), i != 0);
+        }
+        umma_commit(&s_sc[st]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = !FULL || nc == 0 || scores(0);
+    for (int c = 0; ok && c < nc && !*(volatile int*)&s_fail; ++c) {
+      const int st = c & 1;
+      const unsigned par = (unsigned)c & 1u;
+      const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
+      // weighted v is there, and the last update has been read
+      ok = wait(&s_w, par);
+      if (ok && !FULL) ok = wait(&s_full[st], (unsigned)(c >> 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      if (la_elect()) {
+#pragma unroll
+        for (int i = 0; i < kLaT / 16; ++i)
+          umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u, la_idesc(192, true, true), i != 0);
+        umma_commit(&s_kv);
+        if (!FULL) umma_commit(&s_pv[st]);
+      }
+      __syncwarp();
+      if (!FULL) continue;
+      // the outputs of the chunk before have been read
+      if (c > 0) ok = wait(&s_ofree, par ^ 1u);
+      if (ok && c + 1 < nc) ok = scores(c + 1);
+      if (ok) ok = wait(&s_b, par);  // the state's copy is there
+      if (!ok) break;
+      tc_fence_after();
+      if (la_elect()) {
+#pragma unroll
+        for (int i = 0; i < KD / 16; ++i)
+          umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
+                      la_idesc(64, false, true), i != 0);
+        umma_commit(&s_qs);
+      }
+      __syncwarp();
+      ok = wait(&s_p, par);
+      if (!ok) break;
+      tc_fence_after();
+      if (la_elect()) {
+#pragma unroll
+        for (int i = 0; i < kLaT / 16; ++i)
+          umma_f16_ts(t_sc + 128 * st + 64, t_sc + 128 * st + i * 8,
+                      dv0 + st * (kLaBlk >> 4) + i * 128u, la_idesc(64, false, true), i != 0);
+        umma_commit(&s_pv[st]);
+      }
+      __syncwarp();
+    }
+    if (!ok) s_fail = 1;
+    // every product has completed before the TMEM is given back
+    if (la_elect()) umma_commit(&s_drain);
+    __syncwarp();
+    WaitCtx last = wctx;
+    if (last.timeout_ns < 2000000000LL) last.timeout_ns = 2000000000LL;
+    la_wait(&s_drain, 0u, last);
+  } else if (warp < 10) {
+    // ---- weighted scores and outputs: thread = token, half of the columns -----------
+    const int i = row;
+    const long long obase = (long long)b * a.ob + (long long)h * a.oh + col0;
+    const int nd = a.dv - col0 < kLaN ? a.dv - col0 : kLaN;
+    const bool whole = a.o_f32 || (a.dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31) == 0);
+    const float* wt0 = s_wt + (rev ? 32 - i : 127 - i);
+    for (int c = 0; FULL && c < nc; ++c) {
+      const int st = c & 1;
+      const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
+      const int n = rows(c);
+      bool ok = la_wait(&s_sc[st], par2, wctx);
+      if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+        s_fail = 1;
+        break;
+      }
+      tc_fence_after();
+      const unsigned t_s = t_sc + lane_off + 128 * st;
+      // two blocks of 32 columns; those beyond the diagonal block J = qd are zero
+      unsigned w[32];
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        const int J = 2 * hf + jj;
+        if (rev ? J >= qd : J <= qd) {  // uniform in the warp
+          unsigned r[32];
+          tmem_ld16_async(t_s + 32 * J, r);
+          tmem_ld16_async(t_s + 32 * J + 16, r + 16);
+          float f[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) f[e] = wt0[32 * J + e];
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[16 * jj + e] = pack_bf16(__uint_as_float(r[2 * e]) * f[2 * e],
+                                       __uint_as_float(r[2 * e + 1]) * f[2 * e + 1]);
+          if (32 * J + 32 > n) {  // a score of the last chunk's padding may be anything
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int left = n - 32 * J - 2 * e;
+              w[16 * jj + e] = left <= 0 ? 0u : (left == 1 ? w[16 * jj + e] & 0xFFFFu : w[16 * jj + e]);
+            }
           }
-          umma_commit(&s_sc);
-          ok = stage_wait(&s_b, par, wctx);  // weighted v and the state's copy are there
-        }
-        if (ok) {
-          tc_fence_after();
+        } else {
 #pragma unroll
-          for (int i = 0; i < kLaT / 16; ++i)
-            umma_f16_ss(t_kv, umma_desc_mn_sw128(k + i * 2048u),
-                        umma_desc_mn_sw128(sbase + Sm::kVw + i * 2048u),
-                        la_idesc(192, true, true), i != 0);
-          umma_commit(&s_kv);
-          // the outputs of the chunk before have been read
-          if (c > 0) ok = stage_wait(&s_ofree, par ^ 1u, wctx);
+          for (int e = 0; e < 16; ++e) w[16 * jj + e] = 0u;
         }
-        if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < KD / 16; ++i)
-            umma_f16_ss(t_oi, umma_desc_sw128(q + (i >> 2) * kLaBlk + (i & 3) * 32u),
-                        umma_desc_mn_sw128(sbase + Sm::kS + i * 2048u),
-                        la_idesc(64, false, true), i != 0);
-          umma_commit(&s_qs);
-          ok = stage_wait(&s_p, par, wctx);
-        }
-        if (!ok) {
+      }
+      // the weighted scores go to columns 0-63, where the warp of the lower half reads
+      tc_fence_before();
+      if (hf == 0) {
+        mbar_arrive(&s_rd[qd]);
+      } else {
+        ok = la_wait(&s_rd[qd], par, wctx);
+        if (!__all_sync(0xffffffffu, ok)) {
           s_fail = 1;
           break;
         }
         tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < kLaT / 16; ++i)
-          umma_f16_ts(t_oa, t_p + i * 8, umma_desc_mn_sw128(v + i * 2048u),
-                      la_idesc(64, false, true), i != 0);
-        umma_commit(&s_pv[st]);
       }
-      // every product has completed before the TMEM is given back
-      umma_commit(&s_drain);
-      WaitCtx last = wctx;
-      if (last.timeout_ns < 2000000000LL) last.timeout_ns = 2000000000LL;
-      stage_wait(&s_drain, 0u, last);
-    }
-  } else if (warp < 6) {
-    // ---- weighted scores and outputs: thread = token -------------------------------
-    const int qd = warp & 3, i = 32 * qd + lane;
-    const unsigned lane_off = (unsigned)(32 * qd) << 16;
-    const float cs = a.c_out * a.c_kv;
-    const long long obase = (long long)b * a.ob + (long long)h * a.oh + col0;
-    const int nd = a.dv - col0 < kLaN ? a.dv - col0 : kLaN;
-    for (int c = 0; c < nc; ++c) {
-      const unsigned par = (unsigned)c & 1u;
-      const int n = rows(c);
-      bool ok = stage_wait(&s_sc, par, wctx);
-      if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
-        s_fail = 1;
-        break;
-      }
-      tc_fence_after();
-#pragma unroll 1
-      for (int J = 0; J < 4; ++J) {
-        unsigned w[16];
-        const bool live = rev ? J >= qd : J <= qd;  // uniform in the warp
-        if (live) {
-          unsigned r[32];
-          tmem_ld32_async(t_sc + lane_off + 32 * J, r);
-          tmem_wait_ld();
-          if (J == qd) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x[2];
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const int d = rev ? e + g - lane : lane - e - g;
-                const float f = s_pw[d & 127] * cs;
-                x[g] = d >= 0 && 32 * J + e + g < n ? __uint_as_float(r[e + g]) * f : 0.0f;
-              }
-              w[e / 2] = pack_bf16(x[0], x[1]);
-            }
-          } else {
-            const float f = cs * s_pw[rev ? 32 * J - i : i - 32 * J - 31];
-            const int m = n - 32 * J;  // columns at and after m are padding
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(&s_col[e]);
-              float x[4] = {__uint_as_float(r[e]) * (f * cf.x),
-                            __uint_as_float(r[e + 1]) * (f * cf.y),
-                            __uint_as_float(r[e + 2]) * (f * cf.z),
-                            __uint_as_float(r[e + 3]) * (f * cf.w)};
-              if (m < 32) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                  if (e + g >= m) x[g] = 0.0f;
-              }
-              w[e / 2] = pack_bf16(x[0], x[1]);
-              w[e / 2 + 1] = pack_bf16(x[2], x[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = 0u;
-        }
-        tmem_st16(t_p + lane_off + 16 * J, w);
-      }
+      tmem_st16(t_s + 32 * hf, w);
+      tmem_st16(t_s + 32 * hf + 16, w + 16);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&s_p);
 
-      ok = stage_wait(&s_pv[c & 1], (unsigned)(c >> 1) & 1u, wctx);
+      ok = la_wait(&s_pv[st], par2, wctx);
       if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
         s_fail = 1;
         break;
       }
       tc_fence_after();
+      unsigned y[32];
+      tmem_ld16_async(t_oi + lane_off + 32 * hf, y);
+      tmem_ld16_async(t_s + 64 + 32 * hf, w);
+      tmem_ld16_async(t_oi + lane_off + 32 * hf + 16, y + 16);
+      tmem_ld16_async(t_s + 64 + 32 * hf + 16, w + 16);
       const float e = i < n ? a.c_out * s_pw[rev ? n - 1 - i : i + 1] : 0.0f;
-      float x[64];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        unsigned y[32], w[32];
-        tmem_ld32_async(t_oi + lane_off + 32 * half, y);
-        tmem_ld32_async(t_oa + lane_off + 32 * half, w);
-        tmem_wait_ld();
-#pragma unroll
-        for (int d = 0; d < 32; ++d)
-          x[32 * half + d] = fmaf(e, __uint_as_float(y[d]), __uint_as_float(w[d]));
-      }
+      const f32x2 ee = pair2(e, e);
+      tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&s_ofree);
+      f32x2 x[16];
+#pragma unroll
+      for (int d = 0; d < 16; ++d)
+        x[d] = fma2(ee, pair2u(y[2 * d], y[2 * d + 1]), pair2u(w[2 * d], w[2 * d + 1]));
+      const long long at = obase + (long long)(t0(c) + i) * a.ot + 32 * hf;
       if (i < n) {
-        const long long at = obase + (long long)(t0(c) + i) * a.ot;
         if (a.o_f32) {
           float* o = static_cast<float*>(a.o) + at;
 #pragma unroll
-          for (int d = 0; d < 64; d += 4)
-            if (d < nd)
-              *reinterpret_cast<float4*>(o + d) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
+          for (int d = 0; d < 32; d += 8)
+            if (32 * hf + d < nd) {
+              unsigned u[8];
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                u[2 * g] = (unsigned)x[d / 2 + g];
+                u[2 * g + 1] = (unsigned)(x[d / 2 + g] >> 32);
+              }
+              stg256(o + d, true, u);
+            }
         } else {
           __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + at;
 #pragma unroll
-          for (int d = 0; d < 64; d += 8)
-            if (d < nd)
-              *reinterpret_cast<uint4*>(o + d) =
-                  make_uint4(pack_bf16(x[d], x[d + 1]), pack_bf16(x[d + 2], x[d + 3]),
-                             pack_bf16(x[d + 4], x[d + 5]), pack_bf16(x[d + 6], x[d + 7]));
+          for (int d = 0; d < 32; d += 16) {
+            unsigned u[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              float x0, x1;
+              unpair2(x[d / 2 + g], x0, x1);
+              u[g] = pack_bf16(x0, x1);
+            }
+            if (32 * hf + d + 8 < nd)
+              stg256(o + d, whole, u);
+            else if (32 * hf + d < nd)
+              *reinterpret_cast<uint4*>(o + d) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
         }
       }
     }
-    if (p.zero_tail && !*(volatile int*)&s_fail) {
-      for (long long t = len + i; t < p.L; t += kLaT)
-        for (int d = 0; d < nd; d += 8) {
+    if (FULL && p.zero_tail && !*(volatile int*)&s_fail) {
+      const long long end = span == p.nspan - 1 ? p.L : tb + p.span;
+      for (long long t = tb + len + i; t < end; t += kLaT)
+        for (int d = 8 * hf; d < nd; d += 16) {
           const long long at = obase + t * a.ot + d;
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           if (a.o_f32) {
@@ -414,105 +564,140 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
     }
   } else {
-    // ---- weighted v and the state: thread = token, thread = state row --------------
-    const int qd = warp & 3, r = 32 * qd + lane;
-    const unsigned lane_off = (unsigned)(32 * qd) << 16;
-    const bool srow = r < a.dk;
-    const long long sb = ((long long)b * p.H + h) * a.dk * a.dv;
-    float s[kLaN];
+    // ---- the state and weighted v: thread = state row = token, half of the columns -----
+    const int r = row;
 #pragma unroll
-    for (int d = 0; d < kLaN; ++d) s[d] = 0.0f;
-    if (a.s_in && srow) {
+    for (int d = 0; d < 16; ++d) s[d] = 0;
+    if (s_in && r < a.dk) {
 #pragma unroll
-      for (int d = 0; d < kLaN; ++d)
-        if (col0 + d < a.dv) s[d] = a.s_in[sb + r * a.s_r + (col0 + d) * a.s_c];
+      for (int d = 0; d < 32; d += 2)
+        if (cs0 + d < a.dv) {
+          const float* sp = s_in + sb + r * sr + (cs0 + d) * sc;
+          s[d / 2] = pair2(sp[0], sp[sc]);
+        }
     }
     float ghi, glo;  // gamma^128
     la_two(la_pow(ld, kLaT), ghi, glo);
-    bool failed = false;
-    // s <- gamma^m s + U of the chunk before, which had m tokens
-    const auto take = [&](int c) {
-      bool ok = stage_wait(&s_kv, (unsigned)c & 1u, wctx);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      tc_fence_after();
-      float h1 = ghi, h2 = glo;
-      const int m = rows(c);
-      if (m < kLaT) la_two(la_pow(ld, m), h1, h2);
+    const float vfull = a.c_kv * s_pw[rev ? r + 1 : kLaT - 1 - r];
+    const unsigned wb = sbase + Sm::kVw;
+    bool ok = true;
+    for (int c = 0; c <= nc; ++c) {
+      const int st = c & 1;
+      if (c > 0) {
+        // s <- gamma^m s + U of the chunk before, which had m tokens
+        ok = la_wait(&s_kv, (unsigned)(c - 1) & 1u, wctx);
+        if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float h1 = ghi, h2 = glo;
+        const int m = rows(c - 1);
+        if (m < kLaT) la_two(la_pow(ld, m), h1, h2);
+        const f32x2 hh1 = pair2(h1, h1), hh2 = pair2(h2, h2);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        unsigned u1[32], u2[32], u3[32];
-        tmem_ld32_async(t_kv + lane_off + 32 * half, u1);
-        tmem_ld32_async(t_kv + lane_off + 64 + 32 * half, u2);
-        tmem_ld32_async(t_kv + lane_off + 128 + 32 * half, u3);
-        tmem_wait_ld();
+        for (int part = 0; part < 2; ++part) {
+          unsigned u1[16], u2[16], u3[16];
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 16 * part, u1);
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 64 + 16 * part, u2);
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 128 + 16 * part, u3);
+          tmem_wait_ld();
 #pragma unroll
-        for (int d = 0; d < 32; ++d) {
-          const float old = s[32 * half + d];
-          const float small = fmaf(h2, old, __uint_as_float(u3[d]) + __uint_as_float(u2[d]));
-          s[32 * half + d] = fmaf(h1, old, __uint_as_float(u1[d]) + small);
+          for (int d = 0; d < 8; ++d) {
+            const f32x2 old = s[8 * part + d];
+            const f32x2 low = fma2(
+                hh2, old, add2(pair2u(u3[2 * d], u3[2 * d + 1]), pair2u(u2[2 * d], u2[2 * d + 1])));
+            s[8 * part + d] = fma2(hh1, old, add2(pair2u(u1[2 * d], u1[2 * d + 1]), low));
+          }
         }
       }
-      return true;
-    };
-    for (int c = 0; c < nc; ++c) {
-      const int st = c & 1, n = rows(c);
-      if (c > 0 && !take(c - 1)) {
-        failed = true;
-        break;
-      }
-      bool ok = true;
-      if (c > 0) ok = stage_wait(&s_qs, (unsigned)(c - 1) & 1u, wctx);  // the copy has been read
-      if (ok) ok = stage_wait(&s_full[st], (unsigned)(c >> 1) & 1u, wctx);
+      if (c == nc) break;
+      const int n = rows(c);
+      ok = la_wait(&s_vfull[st], (unsigned)(c >> 1) & 1u, wctx);
+      if (ok && n < kLaT) ok = la_wait(&s_full[st], (unsigned)(c >> 1) & 1u, wctx);
       if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
-        failed = true;
+        ok = false;
         break;
       }
-      if (KD == 128 || r < KD) {
+      const unsigned vb = sbase + Sm::kV + st * kLaBlk;
+      float f = vfull;
+      if (n < kLaT) {
+        f = r < n ? a.c_kv * s_pw[rev ? r + 1 : n - 1 - r] : 0.0f;
+        if (r >= n) {  // padding of v and k: whatever it holds becomes zero
+#pragma unroll 1
+          for (int j = 4 * hf; j < 4 * hf + 4; ++j) {
+            sts128(la_unit(vb, r, j), 0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          sts128(la_unit(sbase + Sm::kS, r, j), pack_bf16(s[8 * j], s[8 * j + 1]),
-                 pack_bf16(s[8 * j + 2], s[8 * j + 3]), pack_bf16(s[8 * j + 4], s[8 * j + 5]),
-                 pack_bf16(s[8 * j + 6], s[8 * j + 7]));
+            for (int m = 0; m < KD / 64; ++m)
+              sts128(la_unit(sbase + Sm::kK + (st * (KD / 64) + m) * kLaBlk, r, j), 0u, 0u, 0u, 0u);
+          }
+        }
       }
-      const unsigned vb = sbase + Sm::kV + st * kLaBlk, wb = sbase + Sm::kVw;
-      const float f = r < n ? a.c_kv * s_pw[rev ? r + 1 : n - 1 - r] : 0.0f;
+      const f32x2 ff = pair2(f, f), minus = pair2(-1.0f, -1.0f);
+#pragma unroll 1
+      for (int j = 4 * hf; j < 4 * hf + 4; j += 2) {
+        const uint4 x0 = lds128(la_unit(vb, r, j)), x1 = lds128(la_unit(vb, r, j + 1));
+        const unsigned in[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        unsigned w1[8], w2[8], w3[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint4 x = lds128(la_unit(vb, r, j));
-        if (r >= n) {  // padding: whatever it holds becomes zero, in k too
-          x = make_uint4(0u, 0u, 0u, 0u);
-          sts128(la_unit(vb, r, j), 0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int m = 0; m < KD / 64; ++m)
-            sts128(la_unit(sbase + Sm::kK + (st * (KD / 64) + m) * kLaBlk, r, j), 0u, 0u, 0u, 0u);
-        }
-        const unsigned in[4] = {x.x, x.y, x.z, x.w};
-        unsigned w1[4], w2[4], w3[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float y0 = bf16_lo(in[g]) * f, y1 = bf16_hi(in[g]) * f;
+        for (int g = 0; g < 8; ++g) {
+          const f32x2 y = mul2(pair2(bf16_lo(in[g]), bf16_hi(in[g])), ff);
+          float y0, y1, z0, z1;
+          unpair2(y, y0, y1);
           w1[g] = pack_bf16(y0, y1);
-          const float z0 = y0 - bf16_lo(w1[g]), z1 = y1 - bf16_hi(w1[g]);
+          const f32x2 z = fma2(pair2(bf16_lo(w1[g]), bf16_hi(w1[g])), minus, y);
+          unpair2(z, z0, z1);
           w2[g] = pack_bf16(z0, z1);
-          w3[g] = pack_bf16(z0 - bf16_lo(w2[g]), z1 - bf16_hi(w2[g]));
+          unpair2(fma2(pair2(bf16_lo(w2[g]), bf16_hi(w2[g])), minus, z), z0, z1);
+          w3[g] = pack_bf16(z0, z1);
         }
-        sts128(la_unit(wb, r, j), w1[0], w1[1], w1[2], w1[3]);
-        sts128(la_unit(wb + kLaBlk, r, j), w2[0], w2[1], w2[2], w2[3]);
-        sts128(la_unit(wb + 2 * kLaBlk, r, j), w3[0], w3[1], w3[2], w3[3]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          sts128(la_unit(wb, r, j + g), w1[4 * g], w1[4 * g + 1], w1[4 * g + 2], w1[4 * g + 3]);
+          sts128(la_unit(wb + kLaBlk, r, j + g), w2[4 * g], w2[4 * g + 1], w2[4 * g + 2],
+                 w2[4 * g + 3]);
+          sts128(la_unit(wb + 2 * kLaBlk, r, j + g), w3[4 * g], w3[4 * g + 1], w3[4 * g + 2],
+                 w3[4 * g + 3]);
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
+      mbar_arrive(&s_w);
+      if (!FULL) continue;
+      if (c > 0) {  // the last copy of the state has been read
+        ok = la_wait(&s_qs, (unsigned)(c - 1) & 1u, wctx);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+      }
+      if (KD == 128 || r < KD) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          unsigned u[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float x0, x1;
+            unpair2(s[4 * j + g], x0, x1);
+            u[g] = pack_bf16(x0, x1);
+          }
+          sts128(la_unit(sbase + Sm::kS, r, 4 * hf + j), u[0], u[1], u[2], u[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(&s_b);
     }
-    if (!failed && nc > 0 && !take(nc - 1)) failed = true;
-    if (failed) {
+    if (!ok) {
       s_fail = 1;
-    } else if (a.s_out && srow) {
+    } else if (FULL && r < a.dk) {
+      bool fine = true;
 #pragma unroll
-      for (int d = 0; d < kLaN; d += 4)
-        if (col0 + d < a.dv)
-          *reinterpret_cast<float4*>(a.s_out + sb + (long long)r * a.dv + col0 + d) =
-              make_float4(s[d], s[d + 1], s[d + 2], s[d + 3]);
+      for (int d = 0; d < 16; ++d) {
+        float x0, x1;
+        unpair2(s[d], x0, x1);
+        fine = fine && isfinite(x0) && isfinite(x1);  // columns past dv are sums of zeros
+      }
+      if (!fine) s_bad = 1;
     }
   }
 
@@ -524,6 +709,48 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
+  }
+  if (s_fail) return;
+  if (FULL && s_bad) {
+    if (threadIdx.x < kLaAgainThreads)
+      la_walk<__nv_bfloat16, kLaN, kLaAgainThreads>(
+          p, a, b, h, col0, tb, len, s_in ? s_in + sb : nullptr, sr, sc,
+          s_out ? s_out + sb : nullptr, *reinterpret_cast<LaWalkSmem<kLaN>*>(dsmem));
+  } else if (warp >= 10 && s_out && row < a.dk) {
+#pragma unroll
+    for (int d = 0; d < 32; d += 4)
+      if (cs0 + d < a.dv) {
+        float4 x;
+        unpair2(s[d / 2], x.x, x.y);
+        unpair2(s[d / 2 + 1], x.z, x.w);
+        *reinterpret_cast<float4*>(s_out + sb + (long long)row * a.dv + cs0 + d) = x;
+      }
+  }
+}
+
+// The states that the spans' own tokens leave (s_span, [B, H, spans, dk, dv]) become the
+// states before the spans; the state behind the last one goes to s_out.
+__global__ void pararnn_linattn_join_kernel(const __grid_constant__ LaParams p) {
+  const LaPass& a = p.pass[blockIdx.z];
+  const int bh = blockIdx.x, b = bh / p.H;
+  const float ld = p.log_decay[bh % p.H];
+  const int n = a.dk * a.dv;
+  float ghi, glo;  // of a whole span
+  la_two(la_powl(ld, p.span), ghi, glo);
+  for (int e = threadIdx.x + blockIdx.y * blockDim.x; e < n; e += blockDim.x * gridDim.y) {
+    const int r = e / a.dv, c = e % a.dv;
+    float x = a.s_in ? a.s_in[(long long)bh * n + r * a.s_r + c * a.s_c] : 0.0f;
+    float* sp = a.s_span + (long long)bh * p.nspan * n + e;
+    for (int k = 0; k < p.nspan; ++k) {
+      const int g = a.rev ? p.nspan - 1 - k : k;
+      const long long m = la_span_tokens(p, b, g);
+      float h1 = ghi, h2 = glo;
+      if (m != p.span) la_two(la_powl(ld, m), h1, h2);
+      const float own = sp[(long long)g * n];
+      sp[(long long)g * n] = x;
+      x = m == 0 ? x : fmaf(h1, x, fmaf(h2, x, own));
+    }
+    if (a.s_out) a.s_out[(long long)bh * n + e] = x;
   }
 }
 

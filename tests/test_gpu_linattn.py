@@ -348,3 +348,57 @@ def test_layer_of_operators(pr):
     check_backward(pr, x, dict(do=f(do), ds=None), hd ** -0.5,
                    (dq, dk, dv_, pr.scan_linattn_backward(q, k, v, dev(lam), do,
                                                           scale=hd ** -0.5)[3]))
+
+
+@pytest.mark.parametrize("L", [100, 300, 2000])
+@pytest.mark.parametrize("form", ["recurrent", "chunks"])
+def test_non_finite_tokens_do_not_reach_back(pr, form, L):
+    """A NaN or infinity in one token's k, v or q changes nothing before that token
+    (gradients: nothing that does not depend on it), whatever chunk it lies in."""
+    x, y = make(1, L, 3, 3, 3, 3, 64, 64, seed=15, state=False)
+    x["log_decay"] = np.array([-0.01, -0.3, 0.0])
+    opts = pr.Options(regime=FORMS[form])
+    g, do = on_gpu(x), dev(y["do"], BF)
+    clean = pr.scan_linattn(**g, opts=opts)
+    t = L - 40
+    for name, bad in (("v", float("nan")), ("k", float("inf")), ("v", float("-inf")), ("q", float("nan"))):
+        h = {n: (a.clone() if n in "qkv" else a) for n, a in g.items()}
+        h[name][0, t, 1, 5] = bad
+        o, s = pr.scan_linattn(**h, opts=opts)
+        # the chunked form walks such a head again in the recurrent form: other roundings
+        assert torch.equal(o[:, :, ::2], clean[0][:, :, ::2])
+        assert torch.equal(s[:, ::2], clean[1][:, ::2])
+        assert o[:, :t].isfinite().all()
+        bound = 2.0 ** -6 * clean[0].float().abs().max()
+        assert (o[:, :t].float() - clean[0][:, :t].float()).abs().max() <= bound
+        if name == "q":
+            assert s.isfinite().all() and o[:, t + 1:].isfinite().all()
+            assert not o[0, t, 1].isfinite().any()
+        elif name == "v":
+            assert not o[0, t:, 1, 5].isfinite().any() and not s[0, 1, :, 5].isfinite().any()
+            keep = [i for i in range(64) if i != 5]
+            assert o[0, t:, 1, keep].isfinite().all()
+        else:
+            assert not o[0, t:, 1].isfinite().any()
+        # dq_t depends on k and v up to t, dv_t and dk_t on q and do from t on
+        dq, dk, dv, ds0 = pr.scan_linattn_backward(**h, do=do, opts=opts)
+        if name != "q":
+            assert dq[0, :t].isfinite().all()
+        else:
+            assert dq.isfinite().all() and dk[0, t + 1:].isfinite().all()
+            assert dv[0, t + 1:].isfinite().all()
+
+
+def test_a_state_that_is_not_finite(pr):
+    x, _ = make(1, 200, 2, 2, 2, 2, 64, 64, seed=16)
+    x["log_decay"] = np.array([-0.1, -0.1])
+    g = on_gpu(x)
+    g["s0"][0, 1, 3, 7] = float("nan")
+    before = g["s0"].clone()
+    o, s = pr.scan_linattn(**g, state_out=g["s0"])  # in place: walked again from the old state
+    keep = [i for i in range(64) if i != 7]
+    assert o[0, :, 0].isfinite().all() and o[0, :, 1, keep].isfinite().all()
+    assert o[0, :, 1, 7].isnan().all()
+    again = pr.scan_linattn(**dict(g, s0=before))
+    assert torch.equal(again[0].isnan(), o.isnan()) and torch.equal(again[1].isnan(), s.isnan())
+    assert torch.equal(again[0].nan_to_num(), o.nan_to_num())
