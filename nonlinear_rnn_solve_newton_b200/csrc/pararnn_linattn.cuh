@@ -83,7 +83,7 @@ __device__ __forceinline__ void la_two(double x, float& hi, float& lo) {
 }
 
 // gamma^i in 64 bits; gamma^0 = 1 also for gamma = 0
-__device__ __forceinline__ double la_powl(float log_decay, long long i) {
+__device__ __noinline__ inline double la_powl(float log_decay, long long i) {
   return i == 0 ? 1.0 : exp((double)log_decay * (double)i);
 }
 __device__ __forceinline__ double la_pow(float log_decay, int i) { return la_powl(log_decay, i); }
@@ -127,7 +127,7 @@ __device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, 
   // of times, and the half step that one float leaves (2^-25 near 1) would add up
   // in the same direction every time
   float gamma, glow;
-  la_two(exp((double)p.log_decay[h]), gamma, glow);
+  la_two(la_pow(p.log_decay[h], 1), gamma, glow);
 
   float s[R][4];
 #pragma unroll

@@ -21,8 +21,8 @@
 // S that Q multiplies are rounded to bf16: two independent roundings of terms of
 // an output that is itself rounded to bf16.
 //
-// Roles: warp 0 tensor copies (q, k, v of a chunk, two stages), warp 1 issues
-// the products, warps 2-9 weight the scores and write the outputs, warps 10-17
+// Roles: warp 0 tensor copies (q, k, v of a chunk, two stages each; the output
+// tile, staged where the chunk's v was), warp 1 issues the products, warps 2-9 weight the scores and write the outputs, warps 10-17
 // carry the state, weight v and write the state's bf16 copy.  Two warps share a
 // TMEM lane quarter and split its columns: with four warps a role, each
 // instruction was fetched for a single warp of an SM quarter and a third of the
@@ -52,8 +52,12 @@ namespace pararnn {
 
 constexpr int kLaT = 128;  // tokens per chunk
 constexpr int kLaN = 64;   // state columns per CTA
+constexpr int kLaWt2 = kLaT + 32 + 16;  // the second copy of the weights
 constexpr int kLaThreads = 576;
 constexpr int kLaAgainThreads = 512;  // of the recurrent walk over non-finite inputs
+// chunks that are brought into L2 ahead of the copies: a buffer is refilled only when
+// it falls free, too late for the latency of HBM
+constexpr int kLaAhead = 2;
 constexpr unsigned kLaBlk = kLaT * 128;  // a 128-row block of 64 bf16 columns
 
 template <int KD> struct LaSmem {
@@ -67,12 +71,13 @@ template <int KD> struct LaSmem {
 };
 
 struct LaMaps {
-  CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses];
+  CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses], o[kLaMaxPasses];
 };
 
-// stage_wait with a thread that sleeps in the hardware for up to 2 us a try, so
-// that the waiting warps leave the issue slots to the working ones
-__device__ __forceinline__ bool la_try_wait(unsigned long long* bar, unsigned parity) {
+// A wait: one plain try (41 cycles where the phase is over, 90 with a time limit), then
+// tries that sleep in the hardware for up to 2 us each, so that the waiting warps leave
+// the issue slots to the working ones.
+__device__ __forceinline__ bool la_sleep_wait(unsigned long long* bar, unsigned parity) {
   unsigned ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -83,14 +88,19 @@ __device__ __forceinline__ bool la_try_wait(unsigned long long* bar, unsigned pa
       : "memory");
   return ok != 0u;
 }
-__device__ __forceinline__ bool la_wait(unsigned long long* bar, unsigned parity,
-                                        const WaitCtx& w) {
-  if (la_try_wait(bar, parity)) return true;
+// the polling loop is a call: twenty copies of it in the roles' loops would crowd them
+// out of the instruction caches
+__device__ __noinline__ inline bool la_wait_on(unsigned long long* bar, unsigned parity,
+                                               long long timeout_ns) {
   const unsigned long long t0 = globaltimer();
   for (;;) {
-    if (la_try_wait(bar, parity)) return true;
-    if (globaltimer() - t0 > (unsigned long long)w.timeout_ns) return false;
+    if (la_sleep_wait(bar, parity)) return true;
+    if (globaltimer() - t0 > (unsigned long long)timeout_ns) return false;
   }
+}
+__device__ __forceinline__ bool la_wait(unsigned long long* bar, unsigned parity,
+                                        long long timeout_ns) {
+  return mbar_try_wait(bar, parity) || la_wait_on(bar, parity, timeout_ns);
 }
 
 // MN-major operand written by tensor copies with the 128-byte swizzle: rows of
@@ -170,6 +180,23 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const unsigned*>(&t);
 }
+// The box on its way into L2 (nothing waits for it).
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<unsigned long long>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, unsigned src, int x, int y,
+                                             int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<unsigned long long>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // Two fp32 operations in one instruction, on a pair of neighbouring registers.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair2(float x, float y) {
@@ -218,30 +245,19 @@ __device__ __forceinline__ void sts128(unsigned a, unsigned x, unsigned y, unsig
                : "memory");
 }
 
-// 32 bytes to global memory: one store where the address is 32-byte aligned
-__device__ __forceinline__ void stg256(void* p, bool whole, const unsigned* w) {
-  if (whole)
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  else {
-    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
-
-template <int KD, bool FULL>
+template <int KD, bool FULL, bool F32>
 __global__ void __launch_bounds__(kLaThreads, 1)
     pararnn_linattn_chunk_kernel(const __grid_constant__ LaParams p,
                                  const __grid_constant__ LaMaps tm) {
   using Sm = LaSmem<KD>;
   extern __shared__ __align__(1024) unsigned char dsmem[];
-  __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_sc[2], s_rd[4], s_p, s_kv, s_qs,
-      s_b, s_w, s_ofree, s_drain;
-  __shared__ float s_pw[kLaT + 1];        // gamma^i
+  __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_put[2], s_sc[2],
+      s_rd[4], s_p, s_kv[2], s_qs[2], s_b, s_go, s_pad, s_drain;
   // c_out c_kv gamma^d by distance d, in the order in which a row's columns need it:
-  // forwards d = 127 - x, backwards d = x - 32; 0 for the 32 distances below 0
-  __shared__ float s_wt[kLaT + 32];
+  // forwards d = 127 - x, backwards d = x - 32; 0 for the 32 distances below 0.  A second
+  // copy, one place on and 16 banks off, is for rows whose first place is odd: every
+  // row then reads aligned pairs, and no two rows of a half warp the same bank
+  __shared__ __align__(16) float s_wt[2 * (kLaT + 32) + 16];
   __shared__ unsigned s_tmem;
   __shared__ int s_fail, s_bad;
 
@@ -252,11 +268,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int bh = (int)(blockIdx.x / p.nspan), span = (int)(blockIdx.x % p.nspan);
   const int b = bh / p.H, h = bh % p.H;
   const unsigned sbase = (smem_u32(dsmem) + 1023u) & ~1023u;
-  const WaitCtx wctx{nullptr, p.status_dev, p.timeout_ns};
+  const long long limit = p.timeout_ns;
   // the tokens of this CTA: [tb, tb + len)
-  const long long tb = span * p.span;
-  const long long len = la_span_tokens(p, b, span);
-  const int nc = (int)((len + kLaT - 1) / kLaT);
+  const int tb = (int)(span * p.span), len = (int)la_span_tokens(p, b, span);  // L < 2^31
+  const int nc = (len + kLaT - 1) / kLaT;
   const float ld = p.log_decay[h];
   const bool rev = a.rev != 0;
   // the state before this span and behind it: element (r, c) at r s_r + c s_c
@@ -267,19 +282,20 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
+      mbar_init(&s_full[s], FULL ? 2 : 1);
       mbar_init(&s_vfull[s], 1);
+      mbar_init(&s_kv[s], 1);
+      mbar_init(&s_qs[s], 1);
       mbar_init(&s_pv[s], 1);
+      mbar_init(&s_put[s], 256);
       mbar_init(&s_sc[s], 1);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&s_rd[s], 32);
-    mbar_init(&s_kv, 1);
-    mbar_init(&s_qs, 1);
     mbar_init(&s_drain, 1);
     mbar_init(&s_p, 256);
     mbar_init(&s_b, 256);
-    mbar_init(&s_w, 256);
-    mbar_init(&s_ofree, 256);
+    mbar_init(&s_pad, 256);
+    mbar_init(&s_go, FULL ? 512 : 256);
     s_fail = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -292,13 +308,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (threadIdx.x >= 64 && threadIdx.x < 64 + kLaT + 1) {
-    const int i = (int)threadIdx.x - 64;
-    const float g = (float)la_pow(ld, i);
-    s_pw[i] = g;
-    if (i < kLaT) s_wt[rev ? 32 + i : 127 - i] = a.c_out * a.c_kv * g;
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + kLaT) {
+    const int i = (int)threadIdx.x - 64, x = rev ? 32 + i : 127 - i;
+    const float g = a.c_out * a.c_kv * (float)la_pow(ld, i);
+    s_wt[x] = g;
+    if (x > 0) s_wt[kLaWt2 + x - 1] = g;
   } else if (threadIdx.x >= 256 && threadIdx.x < 288) {
-    s_wt[threadIdx.x - 256 + (rev ? 0 : kLaT)] = 0.0f;
+    const int x = (int)threadIdx.x - 256 + (rev ? 0 : kLaT);
+    s_wt[x] = 0.0f;
+    if (x > 0) s_wt[kLaWt2 + x - 1] = 0.0f;
   }
   tc_fence_before();
   __syncthreads();
@@ -306,10 +324,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const unsigned tmem = s_tmem;
   const unsigned t_sc = tmem, t_kv = tmem + 256, t_oi = tmem + 448;
   // token of row 0 of the c-th chunk walked, and its number of tokens
-  const auto t0 = [&](int c) { return (int)tb + (rev ? nc - 1 - c : c) * kLaT; };
-  const auto rows = [&](int c) {
-    return (int)(tb + len - t0(c) < kLaT ? tb + len - t0(c) : kLaT);
-  };
+  const auto t0 = [&](int c) { return tb + (rev ? nc - 1 - c : c) * kLaT; };
+  const int c_tail = rev ? 0 : nc - 1, n_tail = len - (nc - 1) * kLaT;  // the chunk with padding
+  const auto rows = [&](int c) { return c == c_tail ? n_tail : kLaT; };
+
+  // whether a chunk's output goes out as one tensor store: bf16, and no row of the
+  // tile that must stay as it is (the store clips at L itself)
+  const bool tail_staged = n_tail == kLaT || tb + len == p.L, bf16_out = !(F32 && a.o_f32);
+  const auto staged = [&](int c) { return bf16_out && (c != c_tail || tail_staged); };
 
   // the state, and its bf16 copy's halves, belong to warps 10-17
   const int qd = warp & 3, row = 32 * qd + lane, hf = warp < 10 ? (warp - 2) >> 2 : (warp - 10) >> 2;
@@ -322,30 +344,62 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       // ---- tensor copies ----------------------------------------------------------
       const CUtensorMap *mq = &tm.q[blockIdx.z], *mk = &tm.k[blockIdx.z], *mv = &tm.v[blockIdx.z];
       const int hq = h / a.q.rep, hk = h / a.k.rep, hv = h / a.v.rep;
-      int c = 0;
-      for (; c < nc && !*(volatile int*)&s_fail; ++c) {
+      int done = 0;  // chunks whose copies were issued
+      for (int c = 0; c < nc + 2 && !*(volatile int*)&s_fail; ++c) {
         const int st = c & 1;
-        // the products of chunk c - 2 have read this stage
-        if (c >= 2 && !la_wait(&s_pv[st], (unsigned)((c >> 1) - 1) & 1u, wctx)) {
-          s_fail = 1;
-          break;
-        }
-        mbar_expect_tx(&s_full[st], (FULL ? 2 : 1) * (KD / 64) * kLaBlk);
+        const unsigned before = (unsigned)((c >> 1) - 1) & 1u;  // parity of chunk c - 2
+        const unsigned sk = sbase + Sm::kK + st * (KD / 64) * kLaBlk,
+                       sq = sbase + Sm::kQ + st * (KD / 64) * kLaBlk,
+                       sv = sbase + Sm::kV + st * kLaBlk;
+        bool ok = true;
+        // each buffer as soon as chunk c - 2 has no more use for it
+        if (c < nc) {
+          if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
+          if (!ok) break;
+          mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
 #pragma unroll
-        for (int j = 0; j < KD / 64; ++j) {
-          const unsigned off = (st * (KD / 64) + j) * kLaBlk;
-          if (FULL) tma_load_4d_s(sbase + Sm::kQ + off, mq, 64 * j, t0(c), hq, b, &s_full[st]);
-          tma_load_4d_s(sbase + Sm::kK + off, mk, 64 * j, t0(c), hk, b, &s_full[st]);
+          for (int j = 0; j < KD / 64; ++j)
+            tma_load_4d_s(sk + j * kLaBlk, mk, 64 * j, t0(c), hk, b, &s_full[st]);
+          if (FULL) {
+            if (c >= 2) ok = la_wait(&s_qs[st], before, limit);
+            if (!ok) break;
+            mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
+#pragma unroll
+            for (int j = 0; j < KD / 64; ++j)
+              tma_load_4d_s(sq + j * kLaBlk, mq, 64 * j, t0(c), hq, b, &s_full[st]);
+          }
         }
-        mbar_expect_tx(&s_vfull[st], kLaBlk);
-        tma_load_4d_s(sbase + Sm::kV + st * kLaBlk, mv, col0, t0(c), hv, b, &s_vfull[st]);
+        if (FULL && c >= 2) {  // the output of chunk c - 2 lies where its v was
+          ok = la_wait(&s_put[st], before, limit);
+          if (!ok) break;
+          if (staged(c - 2)) {
+            tma_store_4d(&tm.o[blockIdx.z], sv, col0, t0(c - 2), h, b);
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+        }
+        if (c < nc) {
+          mbar_expect_tx(&s_vfull[st], kLaBlk);
+          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          done = c + 1;
+        }
+        if (c + kLaAhead < nc) {
+          const int t = t0(c + kLaAhead);
+#pragma unroll
+          for (int j = 0; j < KD / 64; ++j) {
+            tma_prefetch_4d(mk, 64 * j, t, hk, b);
+            if (FULL) tma_prefetch_4d(mq, 64 * j, t, hq, b);
+          }
+          tma_prefetch_4d(mv, col0, t, hv, b);
+        }
       }
-      // no copy is in flight when the CTA exits (only a failed wait leaves one)
-      WaitCtx last = wctx;
-      if (last.timeout_ns < 2000000000LL) last.timeout_ns = 2000000000LL;
-      for (int i = c - 2 < 0 ? 0 : c - 2; i < c; ++i) {
+      if (done < nc) s_fail = 1;
+      // no copy is in flight when the CTA exits (only a failed wait leaves loads; a k or
+      // q without its v is waited for too, in vain where it was never issued)
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      const long long last = limit < 2000000000LL ? 2000000000LL : limit;
+      for (int i = done - 2 < 0 ? 0 : done - 2; i < (done < nc ? done + 1 : done); ++i) {
         la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
-        la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
+        if (i < done) la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
       }
     }
   } else if (warp == 1) {
@@ -359,48 +413,52 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                              ds = umma_desc_mn_sw128(sbase + Sm::kS);
     // the whole warp waits; true in every lane or in none
     const auto wait = [&](unsigned long long* bar, unsigned parity) {
-      const bool ok = la_wait(bar, parity, wctx);
+      const bool ok = la_wait(bar, parity, limit);
       return __all_sync(0xffffffffu, ok) != 0;
     };
-    const auto scores = [&](int c) {
+    bool ok = true;
+    // one chunk ahead with the scores
+    for (int c = -1; c < nc && !*(volatile int*)&s_fail; ++c) {
       const int st = c & 1;
-      if (!wait(&s_full[st], (unsigned)(c >> 1) & 1u)) return false;
-      tc_fence_after();
-      if (la_elect()) {
-        const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
-#pragma unroll
-        for (int i = 0; i < KD / 16; ++i) {
-          const unsigned off = stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u;
-          umma_f16_ss(t_sc + 128 * st, dq0 + off, dk0 + off, la_idesc(128, false, false), i != 0);
-        }
-        umma_commit(&s_sc[st]);
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = !FULL || nc == 0 || scores(0);
-    for (int c = 0; ok && c < nc && !*(volatile int*)&s_fail; ++c) {
-      const int st = c & 1;
-      const unsigned par = (unsigned)c & 1u;
+      const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
-      // weighted v is there, and the last update has been read
-      ok = wait(&s_w, par);
-      if (ok && !FULL) ok = wait(&s_full[st], (unsigned)(c >> 1) & 1u);
-      if (!ok) break;
-      tc_fence_after();
-      if (la_elect()) {
+      if (c >= 0) {
+        // weighted v is there, the last update and the last outputs have been read
+        ok = wait(&s_go, par);
+        if (ok && !FULL) ok = wait(&s_full[st], par2);
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
 #pragma unroll
-        for (int i = 0; i < kLaT / 16; ++i)
-          umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u, la_idesc(192, true, true), i != 0);
-        umma_commit(&s_kv);
-        if (!FULL) umma_commit(&s_pv[st]);
+          for (int i = 0; i < kLaT / 16; ++i)
+            umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u, la_idesc(192, true, true),
+                        i != 0);
+          umma_commit(&s_kv[st]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       if (!FULL) continue;
-      // the outputs of the chunk before have been read
-      if (c > 0) ok = wait(&s_ofree, par ^ 1u);
-      if (ok && c + 1 < nc) ok = scores(c + 1);
-      if (ok) ok = wait(&s_b, par);  // the state's copy is there
+      if (c + 1 < nc) {
+        const int sn = st ^ 1;
+        const unsigned stn = sn * (KD / 64) * (kLaBlk >> 4);
+        ok = wait(&s_full[sn], (unsigned)((c + 1) >> 1) & 1u);
+        // a chunk's padding is cleared before its scores are made
+        if (ok && rows(c + 1) < kLaT) ok = wait(&s_pad, 0u);
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
+#pragma unroll
+          for (int i = 0; i < KD / 16; ++i) {
+            const unsigned off = stn + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u;
+            umma_f16_ss(t_sc + 128 * sn, dq0 + off, dk0 + off, la_idesc(128, false, false), i != 0);
+          }
+          umma_commit(&s_sc[sn]);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (c < 0) continue;
+      ok = wait(&s_b, par);  // the state's copy is there
       if (!ok) break;
       tc_fence_after();
       if (la_elect()) {
@@ -408,7 +466,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         for (int i = 0; i < KD / 16; ++i)
           umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
                       la_idesc(64, false, true), i != 0);
-        umma_commit(&s_qs);
+        umma_commit(&s_qs[st]);
       }
       __syncwarp();
       ok = wait(&s_p, par);
@@ -427,22 +485,27 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // every product has completed before the TMEM is given back
     if (la_elect()) umma_commit(&s_drain);
     __syncwarp();
-    WaitCtx last = wctx;
-    if (last.timeout_ns < 2000000000LL) last.timeout_ns = 2000000000LL;
+    const long long last = limit < 2000000000LL ? 2000000000LL : limit;
     la_wait(&s_drain, 0u, last);
   } else if (warp < 10) {
     // ---- weighted scores and outputs: thread = token, half of the columns -----------
     const int i = row;
     const long long obase = (long long)b * a.ob + (long long)h * a.oh + col0;
     const int nd = a.dv - col0 < kLaN ? a.dv - col0 : kLaN;
-    const bool whole = a.o_f32 || (a.dv % 16 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31) == 0);
-    const float* wt0 = s_wt + (rev ? 32 - i : 127 - i);
+    const bool f32 = F32 && a.o_f32;
+    // this row's factor of the carried output, in a full chunk and in the last one
+    const float e_full = a.c_out * (float)la_pow(ld, rev ? kLaT - 1 - i : i + 1);
+    const float e_tail =
+        i < n_tail ? a.c_out * (float)la_pow(ld, rev ? n_tail - 1 - i : i + 1) : 0.0f;
+    const int x0 = rev ? 32 - i : 127 - i;
+    const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
+    if (FULL && nc > 0) mbar_arrive(&s_go);  // chunk 0 has no outputs before it
     for (int c = 0; FULL && c < nc; ++c) {
       const int st = c & 1;
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const int n = rows(c);
-      bool ok = la_wait(&s_sc[st], par2, wctx);
-      if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+      bool ok = la_wait(&s_sc[st], par2, limit);
+      if (!__all_sync(0xffffffffu, ok)) {
         s_fail = 1;
         break;
       }
@@ -457,20 +520,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           unsigned r[32];
           tmem_ld16_async(t_s + 32 * J, r);
           tmem_ld16_async(t_s + 32 * J + 16, r + 16);
-          float f[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) f[e] = wt0[32 * J + e];
-          tmem_wait_ld();
+          f32x2 f[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            w[16 * jj + e] = pack_bf16(__uint_as_float(r[2 * e]) * f[2 * e],
-                                       __uint_as_float(r[2 * e + 1]) * f[2 * e + 1]);
-          if (32 * J + 32 > n) {  // a score of the last chunk's padding may be anything
+            f[e] = *reinterpret_cast<const f32x2*>(wt0 + 32 * J + 2 * e);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int left = n - 32 * J - 2 * e;
-              w[16 * jj + e] = left <= 0 ? 0u : (left == 1 ? w[16 * jj + e] & 0xFFFFu : w[16 * jj + e]);
-            }
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1;
+            unpair2(mul2(pair2u(r[2 * e], r[2 * e + 1]), f[e]), y0, y1);
+            w[16 * jj + e] = pack_bf16(y0, y1);
           }
         } else {
 #pragma unroll
@@ -482,7 +541,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       if (hf == 0) {
         mbar_arrive(&s_rd[qd]);
       } else {
-        ok = la_wait(&s_rd[qd], par, wctx);
+        ok = la_wait(&s_rd[qd], par, limit);
         if (!__all_sync(0xffffffffu, ok)) {
           s_fail = 1;
           break;
@@ -495,8 +554,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       tc_fence_before();
       mbar_arrive(&s_p);
 
-      ok = la_wait(&s_pv[st], par2, wctx);
-      if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+      ok = la_wait(&s_pv[st], par2, limit);
+      if (!__all_sync(0xffffffffu, ok)) {
         s_fail = 1;
         break;
       }
@@ -506,56 +565,53 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       tmem_ld16_async(t_s + 64 + 32 * hf, w);
       tmem_ld16_async(t_oi + lane_off + 32 * hf + 16, y + 16);
       tmem_ld16_async(t_s + 64 + 32 * hf + 16, w + 16);
-      const float e = i < n ? a.c_out * s_pw[rev ? n - 1 - i : i + 1] : 0.0f;
+      const float e = c == c_tail ? e_tail : e_full;
       const f32x2 ee = pair2(e, e);
       tmem_wait_ld();
       tc_fence_before();
-      mbar_arrive(&s_ofree);
+      if (c + 1 < nc) mbar_arrive(&s_go);  // chunk c + 1 may write the outputs
       f32x2 x[16];
 #pragma unroll
       for (int d = 0; d < 16; ++d)
         x[d] = fma2(ee, pair2u(y[2 * d], y[2 * d + 1]), pair2u(w[2 * d], w[2 * d + 1]));
-      const long long at = obase + (long long)(t0(c) + i) * a.ot + 32 * hf;
-      if (i < n) {
-        if (a.o_f32) {
-          float* o = static_cast<float*>(a.o) + at;
+      if (staged(c)) {
+        const unsigned ob = sbase + Sm::kV + st * kLaBlk;
 #pragma unroll
-          for (int d = 0; d < 32; d += 8)
-            if (32 * hf + d < nd) {
-              unsigned u[8];
+        for (int d = 0; d < 4; ++d) {
+          unsigned u[4];
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                u[2 * g] = (unsigned)x[d / 2 + g];
-                u[2 * g + 1] = (unsigned)(x[d / 2 + g] >> 32);
-              }
-              stg256(o + d, true, u);
-            }
-        } else {
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + at;
-#pragma unroll
-          for (int d = 0; d < 32; d += 16) {
-            unsigned u[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              float x0, x1;
-              unpair2(x[d / 2 + g], x0, x1);
-              u[g] = pack_bf16(x0, x1);
-            }
-            if (32 * hf + d + 8 < nd)
-              stg256(o + d, whole, u);
-            else if (32 * hf + d < nd)
-              *reinterpret_cast<uint4*>(o + d) = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int g = 0; g < 4; ++g) {
+            float x0, x1;
+            unpair2(x[4 * d + g], x0, x1);
+            u[g] = pack_bf16(x0, x1);
           }
+          sts128(la_unit(ob, i, 4 * hf + d), u[0], u[1], u[2], u[3]);
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else if (i < n) {
+        const long long at = obase + (long long)(t0(c) + i) * a.ot + 32 * hf;
+#pragma unroll
+        for (int d = 0; d < 32; d += 4)
+          if (32 * hf + d < nd) {
+            float4 y4;
+            unpair2(x[d / 2], y4.x, y4.y);
+            unpair2(x[d / 2 + 1], y4.z, y4.w);
+            if (f32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at + d) = y4;
+            else
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at + d) =
+                  make_uint2(pack_bf16(y4.x, y4.y), pack_bf16(y4.z, y4.w));
+          }
       }
+      mbar_arrive(&s_put[st]);
     }
     if (FULL && p.zero_tail && !*(volatile int*)&s_fail) {
       const long long end = span == p.nspan - 1 ? p.L : tb + p.span;
-      for (long long t = tb + len + i; t < end; t += kLaT)
+      for (long long t = (long long)tb + len + i; t < end; t += kLaT)
         for (int d = 8 * hf; d < nd; d += 16) {
           const long long at = obase + t * a.ot + d;
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          if (a.o_f32) {
+          if (f32) {
             *reinterpret_cast<uint4*>(static_cast<float*>(a.o) + at) = zero;
             *reinterpret_cast<uint4*>(static_cast<float*>(a.o) + at + 4) = zero;
           } else {
@@ -578,15 +634,18 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     }
     float ghi, glo;  // gamma^128
     la_two(la_pow(ld, kLaT), ghi, glo);
-    const float vfull = a.c_kv * s_pw[rev ? r + 1 : kLaT - 1 - r];
+    // this row's weight of v, in a full chunk and in the last one
+    const float vfull = a.c_kv * (float)la_pow(ld, rev ? r + 1 : kLaT - 1 - r);
+    const float vtail =
+        r < n_tail ? a.c_kv * (float)la_pow(ld, rev ? r + 1 : n_tail - 1 - r) : 0.0f;
     const unsigned wb = sbase + Sm::kVw;
     bool ok = true;
     for (int c = 0; c <= nc; ++c) {
       const int st = c & 1;
       if (c > 0) {
         // s <- gamma^m s + U of the chunk before, which had m tokens
-        ok = la_wait(&s_kv, (unsigned)(c - 1) & 1u, wctx);
-        if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+        ok = la_wait(&s_kv[st ^ 1], (unsigned)((c - 1) >> 1) & 1u, limit);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
@@ -613,16 +672,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       if (c == nc) break;
       const int n = rows(c);
-      ok = la_wait(&s_vfull[st], (unsigned)(c >> 1) & 1u, wctx);
-      if (ok && n < kLaT) ok = la_wait(&s_full[st], (unsigned)(c >> 1) & 1u, wctx);
-      if (!__all_sync(0xffffffffu, ok) || *(volatile int*)&s_fail) {
+      ok = la_wait(&s_vfull[st], (unsigned)(c >> 1) & 1u, limit);
+      if (ok && n < kLaT) ok = la_wait(&s_full[st], (unsigned)(c >> 1) & 1u, limit);
+      if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       const unsigned vb = sbase + Sm::kV + st * kLaBlk;
       float f = vfull;
       if (n < kLaT) {
-        f = r < n ? a.c_kv * s_pw[rev ? r + 1 : n - 1 - r] : 0.0f;
+        f = vtail;
         if (r >= n) {  // padding of v and k: whatever it holds becomes zero
 #pragma unroll 1
           for (int j = 4 * hf; j < 4 * hf + 4; ++j) {
@@ -662,10 +721,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
-      mbar_arrive(&s_w);
+      mbar_arrive(&s_go);
+      if (FULL && n < kLaT) mbar_arrive(&s_pad);
       if (!FULL) continue;
       if (c > 0) {  // the last copy of the state has been read
-        ok = la_wait(&s_qs, (unsigned)(c - 1) & 1u, wctx);
+        ok = la_wait(&s_qs[st ^ 1], (unsigned)((c - 1) >> 1) & 1u, limit);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
