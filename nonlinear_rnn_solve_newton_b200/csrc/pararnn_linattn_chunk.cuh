@@ -22,7 +22,7 @@
 // an output that is itself rounded to bf16.
 //
 // Roles: warp 0 tensor copies (q, k, v of a chunk, two stages each; the output
-// tile, staged where the chunk's v was), warp 1 issues the products, warps 2-9 weight the scores and write the outputs, warps 10-17
+// tile, staged where the chunk's q was), warp 1 issues the products, warps 2-9 weight the scores and write the outputs, warps 10-17
 // carry the state, weight v and write the state's bf16 copy.  Two warps share a
 // TMEM lane quarter and split its columns: with four warps a role, each
 // instruction was fetched for a single warp of an SM quarter and a third of the
@@ -293,9 +293,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     for (int s = 0; s < 4; ++s) mbar_init(&s_rd[s], 32);
     mbar_init(&s_drain, 1);
     mbar_init(&s_p, 256);
-    mbar_init(&s_b, 256);
+    mbar_init(&s_b, 512);
     mbar_init(&s_pad, 256);
-    mbar_init(&s_go, FULL ? 512 : 256);
+    mbar_init(&s_go, 256);
     s_fail = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                        sq = sbase + Sm::kQ + st * (KD / 64) * kLaBlk,
                        sv = sbase + Sm::kV + st * kLaBlk;
         bool ok = true;
-        // each buffer as soon as chunk c - 2 has no more use for it
+        // each buffer as soon as chunk c - 2 has no more use for it: k, v, then q, where
+        // that chunk's output is staged once its carried product has been made
         if (c < nc) {
           if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
           if (!ok) break;
@@ -360,26 +361,26 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
           for (int j = 0; j < KD / 64; ++j)
             tma_load_4d_s(sk + j * kLaBlk, mk, 64 * j, t0(c), hk, b, &s_full[st]);
+          if (FULL && c >= 2) ok = la_wait(&s_pv[st], before, limit);
+          if (!ok) break;
+          mbar_expect_tx(&s_vfull[st], kLaBlk);
+          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+        }
+        if (FULL && c >= 2) {
+          ok = la_wait(&s_put[st], before, limit);
+          if (!ok) break;
+          if (staged(c - 2)) {
+            tma_store_4d(&tm.o[blockIdx.z], sq, col0, t0(c - 2), h, b);
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+        }
+        if (c < nc) {
           if (FULL) {
-            if (c >= 2) ok = la_wait(&s_qs[st], before, limit);
-            if (!ok) break;
             mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
 #pragma unroll
             for (int j = 0; j < KD / 64; ++j)
               tma_load_4d_s(sq + j * kLaBlk, mq, 64 * j, t0(c), hq, b, &s_full[st]);
           }
-        }
-        if (FULL && c >= 2) {  // the output of chunk c - 2 lies where its v was
-          ok = la_wait(&s_put[st], before, limit);
-          if (!ok) break;
-          if (staged(c - 2)) {
-            tma_store_4d(&tm.o[blockIdx.z], sv, col0, t0(c - 2), h, b);
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          }
-        }
-        if (c < nc) {
-          mbar_expect_tx(&s_vfull[st], kLaBlk);
-          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
           done = c + 1;
         }
         if (c + kLaAhead < nc) {
@@ -394,12 +395,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       if (done < nc) s_fail = 1;
       // no copy is in flight when the CTA exits (only a failed wait leaves loads; a k or
-      // q without its v is waited for too, in vain where it was never issued)
+      // v without its q is waited for too, in vain where it was never issued)
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       const long long last = limit < 2000000000LL ? 2000000000LL : limit;
       for (int i = done - 2 < 0 ? 0 : done - 2; i < (done < nc ? done + 1 : done); ++i) {
         la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
-        if (i < done) la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
+        la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
       }
     }
   } else if (warp == 1) {
@@ -417,13 +418,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       return __all_sync(0xffffffffu, ok) != 0;
     };
     bool ok = true;
-    // one chunk ahead with the scores
+    // Of each chunk the update first (the state's way to the next chunk is the longest),
+    // the two outputs, then the scores of the next chunk, which are weighted while its
+    // update and carried output are made.
     for (int c = -1; c < nc && !*(volatile int*)&s_fail; ++c) {
       const int st = c & 1;
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
       if (c >= 0) {
-        // weighted v is there, the last update and the last outputs have been read
+        // weighted v is there, the last update has been read
         ok = wait(&s_go, par);
         if (ok && !FULL) ok = wait(&s_full[st], par2);
         if (!ok) break;
@@ -436,9 +439,31 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           umma_commit(&s_kv[st]);
         }
         __syncwarp();
+        if (!FULL) continue;
+        ok = wait(&s_b, par);  // the state's copy is there, the last outputs have been read
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
+#pragma unroll
+          for (int i = 0; i < KD / 16; ++i)
+            umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
+                        la_idesc(64, false, true), i != 0);
+          umma_commit(&s_qs[st]);
+        }
+        __syncwarp();
+        ok = wait(&s_p, par);
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
+#pragma unroll
+          for (int i = 0; i < kLaT / 16; ++i)
+            umma_f16_ts(t_sc + 128 * st + 64, t_sc + 128 * st + i * 8,
+                        dv0 + st * (kLaBlk >> 4) + i * 128u, la_idesc(64, false, true), i != 0);
+          umma_commit(&s_pv[st]);
+        }
+        __syncwarp();
       }
-      if (!FULL) continue;
-      if (c + 1 < nc) {
+      if (FULL && c + 1 < nc) {
         const int sn = st ^ 1;
         const unsigned stn = sn * (KD / 64) * (kLaBlk >> 4);
         ok = wait(&s_full[sn], (unsigned)((c + 1) >> 1) & 1u);
@@ -456,30 +481,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
         __syncwarp();
       }
-      if (!ok) break;
-      if (c < 0) continue;
-      ok = wait(&s_b, par);  // the state's copy is there
-      if (!ok) break;
-      tc_fence_after();
-      if (la_elect()) {
-#pragma unroll
-        for (int i = 0; i < KD / 16; ++i)
-          umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
-                      la_idesc(64, false, true), i != 0);
-        umma_commit(&s_qs[st]);
-      }
-      __syncwarp();
-      ok = wait(&s_p, par);
-      if (!ok) break;
-      tc_fence_after();
-      if (la_elect()) {
-#pragma unroll
-        for (int i = 0; i < kLaT / 16; ++i)
-          umma_f16_ts(t_sc + 128 * st + 64, t_sc + 128 * st + i * 8,
-                      dv0 + st * (kLaBlk >> 4) + i * 128u, la_idesc(64, false, true), i != 0);
-        umma_commit(&s_pv[st]);
-      }
-      __syncwarp();
     }
     if (!ok) s_fail = 1;
     // every product has completed before the TMEM is given back
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         i < n_tail ? a.c_out * (float)la_pow(ld, rev ? n_tail - 1 - i : i + 1) : 0.0f;
     const int x0 = rev ? 32 - i : 127 - i;
     const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
-    if (FULL && nc > 0) mbar_arrive(&s_go);  // chunk 0 has no outputs before it
+    if (FULL && nc > 0) mbar_arrive(&s_b);  // chunk 0 has no outputs before it
     for (int c = 0; FULL && c < nc; ++c) {
       const int st = c & 1;
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
@@ -569,13 +570,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const f32x2 ee = pair2(e, e);
       tmem_wait_ld();
       tc_fence_before();
-      if (c + 1 < nc) mbar_arrive(&s_go);  // chunk c + 1 may write the outputs
+      if (c + 1 < nc) mbar_arrive(&s_b);  // chunk c + 1 may write the outputs
       f32x2 x[16];
 #pragma unroll
       for (int d = 0; d < 16; ++d)
         x[d] = fma2(ee, pair2u(y[2 * d], y[2 * d + 1]), pair2u(w[2 * d], w[2 * d + 1]));
       if (staged(c)) {
-        const unsigned ob = sbase + Sm::kV + st * kLaBlk;
+        const unsigned ob = sbase + Sm::kQ + st * (KD / 64) * kLaBlk;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           unsigned u[4];
