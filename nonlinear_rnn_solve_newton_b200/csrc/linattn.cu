@@ -72,19 +72,22 @@ PFN_cuTensorMapEncodeTiled_v12000 la_encoder() {
 
 // A stream [B, L, Hx, D] as a 4-D tensor {D, L, Hx, B}: boxes of 64 columns (one
 // 128-byte swizzle row) x 128 tokens of one head; what lies outside reads as zero.
-bool la_map(CUtensorMap* m, const LaIn& in, int D, const LaParams& lp) {
+bool la_map(CUtensorMap* m, const void* base, long long st, long long sh, long long sb, int D,
+            int Hx, const LaParams& lp) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = la_encoder();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)lp.L, (cuuint64_t)(lp.H / in.rep),
-                              (cuuint64_t)lp.B};
-  const cuuint64_t strides[3] = {(cuuint64_t)in.st * 2, (cuuint64_t)in.sh * 2,
-                                 (cuuint64_t)in.sb * 2};
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)lp.L, (cuuint64_t)Hx, (cuuint64_t)lp.B};
+  const cuuint64_t strides[3] = {(cuuint64_t)st * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
   const cuuint32_t box[4] = {64, kLaT, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(in.p), dims, strides, box,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool la_map(CUtensorMap* m, const LaIn& in, int D, const LaParams& lp) {
+  return la_map(m, in.p, in.st, in.sh, in.sb, D, lp.H / in.rep, lp);
 }
 
 template <int KD, bool FULL, bool F32>
@@ -178,7 +181,8 @@ pararnn_status_t la_launch(LaParams& lp, const LaPlan& pl, float* span_ws,
   for (int i = 0; i < lp.npass; ++i) {
     const LaPass& a = lp.pass[i];
     if (!la_map(&tm.q[i], a.q, a.dk, lp) || !la_map(&tm.k[i], a.k, a.dk, lp) ||
-        !la_map(&tm.v[i], a.v, a.dv, lp))
+        !la_map(&tm.v[i], a.v, a.dv, lp) ||
+        (!a.o_f32 && !la_map(&tm.o[i], a.o, a.ot, a.oh, a.ob, a.dv, lp.H, lp)))
       return PARARNN_ERR_INVALID_ARGUMENT;
     dk = a.dk > dk ? a.dk : dk;
   }

@@ -21,14 +21,14 @@
 // S that Q multiplies are rounded to bf16: two independent roundings of terms of
 // an output that is itself rounded to bf16.
 //
-// Roles: warp 0 tensor copies (q, k, v of a chunk, two stages each), warp 1
-// issues the products, warps 2-9 weight the scores, warps 10-13 write the outputs,
-// warps 14-21 carry the state, weight v and write the state's bf16 copy.  Two
-// warps share a TMEM lane quarter and split its columns where a role has eight:
-// with four, each instruction was fetched for a single warp of an SM quarter and a
-// third of the issue slots waited for instructions.  The scores of the next chunk
-// are made before the outputs of this one, and no role waits for another within a
-// chunk but through the products.  Every wait is bounded.
+// Roles: warp 0 tensor copies (q, k, v of a chunk, two stages each; the output
+// tile, staged where the chunk's v was), warp 1 issues the products, warps 2-9 weight the scores and write the outputs, warps 10-17
+// carry the state, weight v and write the state's bf16 copy.  Two warps share a
+// TMEM lane quarter and split its columns: with four warps a role, each
+// instruction was fetched for a single warp of an SM quarter and a third of the
+// issue slots waited for instructions.  The scores of the next chunk are made
+// before the local output of this one, so that weighting them (the longest step
+// outside the tensor cores) is off the path.  Every wait is bounded.
 //
 // TMEM (512 columns): two buffers of 128 for the scores -- the weighted scores
 // replace the lower half of a buffer, the local output then takes the upper --
@@ -53,7 +53,7 @@ namespace pararnn {
 constexpr int kLaT = 128;  // tokens per chunk
 constexpr int kLaN = 64;   // state columns per CTA
 constexpr int kLaWt2 = kLaT + 32 + 16;  // the second copy of the weights
-constexpr int kLaThreads = 704;
+constexpr int kLaThreads = 576;
 constexpr int kLaAgainThreads = 512;  // of the recurrent walk over non-finite inputs
 // chunks that are brought into L2 ahead of the copies: a buffer is refilled only when
 // it falls free, too late for the latency of HBM
@@ -71,7 +71,7 @@ template <int KD> struct LaSmem {
 };
 
 struct LaMaps {
-  CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses];
+  CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses], o[kLaMaxPasses];
 };
 
 // A wait: one plain try (41 cycles where the phase is over, 90 with a time limit), then
@@ -161,13 +161,6 @@ __device__ __forceinline__ void tmem_ld16_async(unsigned taddr, unsigned* r) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld8_async(unsigned taddr, unsigned* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
-}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -194,6 +187,16 @@ __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, i
                "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, unsigned src, int x, int y,
+                                             int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<unsigned long long>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // Two fp32 operations in one instruction, on a pair of neighbouring registers.
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair2(float x, float y) {
@@ -248,8 +251,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                                  const __grid_constant__ LaMaps tm) {
   using Sm = LaSmem<KD>;
   extern __shared__ __align__(1024) unsigned char dsmem[];
-  __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_sc[2],
-      s_rd[4][2], s_p[2], s_kv[2], s_qs[2], s_b, s_go, s_ofree, s_pad, s_drain;
+  __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_put[2], s_sc[2],
+      s_rd[4], s_p, s_kv[2], s_qs[2], s_b, s_go, s_pad, s_drain;
   // c_out c_kv gamma^d by distance d, in the order in which a row's columns need it:
   // forwards d = 127 - x, backwards d = x - 32; 0 for the 32 distances below 0.  A second
   // copy, one place on and 16 banks off, is for rows whose first place is odd: every
@@ -284,13 +287,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       mbar_init(&s_kv[s], 1);
       mbar_init(&s_qs[s], 1);
       mbar_init(&s_pv[s], 1);
+      mbar_init(&s_put[s], 256);
       mbar_init(&s_sc[s], 1);
-      mbar_init(&s_p[s], 256);
     }
-    for (int s = 0; s < 8; ++s) mbar_init(&s_rd[s >> 1][s & 1], 32);
+    for (int s = 0; s < 4; ++s) mbar_init(&s_rd[s], 32);
     mbar_init(&s_drain, 1);
-    mbar_init(&s_b, 256);
-    mbar_init(&s_ofree, 128);
+    mbar_init(&s_p, 256);
+    mbar_init(&s_b, 512);
     mbar_init(&s_pad, 256);
     mbar_init(&s_go, 256);
     s_fail = 0;
@@ -325,8 +328,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int c_tail = rev ? 0 : nc - 1, n_tail = len - (nc - 1) * kLaT;  // the chunk with padding
   const auto rows = [&](int c) { return c == c_tail ? n_tail : kLaT; };
 
-  // TMEM lane = row, and the half of the columns that this warp has
-  const int qd = warp & 3, row = 32 * qd + lane, hf = warp < 10 ? (warp - 2) >> 2 : (warp - 14) >> 2;
+  // whether a chunk's output goes out as one tensor store: bf16, and no row of the
+  // tile that must stay as it is (the store clips at L itself)
+  const bool tail_staged = n_tail == kLaT || tb + len == p.L, bf16_out = !(F32 && a.o_f32);
+  const auto staged = [&](int c) { return bf16_out && (c != c_tail || tail_staged); };
+
+  // the state, and its bf16 copy's halves, belong to warps 10-17
+  const int qd = warp & 3, row = 32 * qd + lane, hf = warp < 10 ? (warp - 2) >> 2 : (warp - 10) >> 2;
   const unsigned lane_off = (unsigned)(32 * qd) << 16;
   f32x2 s[16];  // 32 columns of state row `row`, from column cs0
   const int cs0 = col0 + 32 * hf;
@@ -341,33 +349,44 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const CUtensorMap *mq = &tm.q[blockIdx.z], *mk = &tm.k[blockIdx.z], *mv = &tm.v[blockIdx.z];
       const int hq = h / a.q.rep, hk = h / a.k.rep, hv = h / a.v.rep;
       int done = 0;  // chunks whose copies were issued
-      for (int c = 0; c < nc && !*(volatile int*)&s_fail; ++c) {
+      for (int c = 0; c < nc + 2 && !*(volatile int*)&s_fail; ++c) {
         const int st = c & 1;
         const unsigned before = (unsigned)((c >> 1) - 1) & 1u;  // parity of chunk c - 2
         const unsigned sk = sbase + Sm::kK + st * (KD / 64) * kLaBlk,
                        sq = sbase + Sm::kQ + st * (KD / 64) * kLaBlk,
                        sv = sbase + Sm::kV + st * kLaBlk;
         bool ok = true;
-        // each buffer as soon as chunk c - 2 has no more use for it
-        if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
-        if (!ok) break;
-        mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
-#pragma unroll
-        for (int j = 0; j < KD / 64; ++j)
-          tma_load_4d_s(sk + j * kLaBlk, mk, 64 * j, t0(c), hk, b, &s_full[st]);
-        if (FULL) {
-          if (c >= 2) ok = la_wait(&s_qs[st], before, limit);
+        // each buffer as soon as chunk c - 2 has no more use for it: k, q, then v, where
+        // that chunk's output is staged
+        if (c < nc) {
+          if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
           if (!ok) break;
           mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
 #pragma unroll
           for (int j = 0; j < KD / 64; ++j)
-            tma_load_4d_s(sq + j * kLaBlk, mq, 64 * j, t0(c), hq, b, &s_full[st]);
-          if (c >= 2) ok = la_wait(&s_pv[st], before, limit);
-          if (!ok) break;
+            tma_load_4d_s(sk + j * kLaBlk, mk, 64 * j, t0(c), hk, b, &s_full[st]);
+          if (FULL) {
+            if (c >= 2) ok = la_wait(&s_qs[st], before, limit);
+            if (!ok) break;
+            mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
+#pragma unroll
+            for (int j = 0; j < KD / 64; ++j)
+              tma_load_4d_s(sq + j * kLaBlk, mq, 64 * j, t0(c), hq, b, &s_full[st]);
+          }
         }
-        mbar_expect_tx(&s_vfull[st], kLaBlk);
-        tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
-        done = c + 1;
+        if (FULL && c >= 2) {
+          ok = la_wait(&s_put[st], before, limit);
+          if (!ok) break;
+          if (staged(c - 2)) {
+            tma_store_4d(&tm.o[blockIdx.z], sv, col0, t0(c - 2), h, b);
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          }
+        }
+        if (c < nc) {
+          mbar_expect_tx(&s_vfull[st], kLaBlk);
+          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          done = c + 1;
+        }
         if (c + kLaAhead < nc) {
           const int t = t0(c + kLaAhead);
 #pragma unroll
@@ -379,8 +398,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       if (done < nc) s_fail = 1;
-      // no copy is in flight when the CTA exits (only a failed wait leaves any; what was
-      // not issued is then waited for in vain)
+      // no copy is in flight when the CTA exits (only a failed wait leaves loads; a k or
+      // v without its q is waited for too, in vain where it was never issued)
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       const long long last = limit < 2000000000LL ? 2000000000LL : limit;
       for (int i = done - 2 < 0 ? 0 : done - 2; i < (done < nc ? done + 1 : done); ++i) {
         la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
@@ -402,13 +422,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       return __all_sync(0xffffffffu, ok) != 0;
     };
     bool ok = true;
+    // Of each chunk the update first (the state's way to the next chunk is the longest),
+    // the two outputs, then the scores of the next chunk, which are weighted while its
+    // update and carried output are made.
     for (int c = -1; c < nc && !*(volatile int*)&s_fail; ++c) {
       const int st = c & 1;
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
-      // the update of chunk c first: the state's way to the next chunk is the longest
       if (c >= 0) {
-        ok = wait(&s_go, par);  // weighted v is there, the last update has been read
+        // weighted v is there, the last update has been read
+        ok = wait(&s_go, par);
         if (ok && !FULL) ok = wait(&s_full[st], par2);
         if (!ok) break;
         tc_fence_after();
@@ -420,11 +443,31 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           umma_commit(&s_kv[st]);
         }
         __syncwarp();
+        if (!FULL) continue;
+        ok = wait(&s_b, par);  // the state's copy is there, the last outputs have been read
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
+#pragma unroll
+          for (int i = 0; i < KD / 16; ++i)
+            umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
+                        la_idesc(64, false, true), i != 0);
+          umma_commit(&s_qs[st]);
+        }
+        __syncwarp();
+        ok = wait(&s_p, par);
+        if (!ok) break;
+        tc_fence_after();
+        if (la_elect()) {
+#pragma unroll
+          for (int i = 0; i < kLaT / 16; ++i)
+            umma_f16_ts(t_sc + 128 * st + 64, t_sc + 128 * st + i * 8,
+                        dv0 + st * (kLaBlk >> 4) + i * 128u, la_idesc(64, false, true), i != 0);
+          umma_commit(&s_pv[st]);
+        }
+        __syncwarp();
       }
-      if (!FULL) continue;
-      if (c > 0) ok = wait(&s_ofree, par ^ 1u);  // the outputs of chunk c - 1 have been read
-      // the scores of chunk c + 1
-      if (ok && c + 1 < nc) {
+      if (FULL && c + 1 < nc) {
         const int sn = st ^ 1;
         const unsigned stn = sn * (KD / 64) * (kLaBlk >> 4);
         ok = wait(&s_full[sn], (unsigned)((c + 1) >> 1) & 1u);
@@ -442,31 +485,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
         __syncwarp();
       }
-      if (!ok) break;
-      if (c < 0) continue;
-      // the outputs of chunk c
-      ok = wait(&s_b, par);  // the state's copy is there
-      if (!ok) break;
-      tc_fence_after();
-      if (la_elect()) {
-#pragma unroll
-        for (int i = 0; i < KD / 16; ++i)
-          umma_f16_ss(t_oi, dq0 + stq + (i >> 2) * (kLaBlk >> 4) + (i & 3) * 2u, ds + i * 128u,
-                      la_idesc(64, false, true), i != 0);
-        umma_commit(&s_qs[st]);
-      }
-      __syncwarp();
-      ok = wait(&s_p[st], par2);
-      if (!ok) break;
-      tc_fence_after();
-      if (la_elect()) {
-#pragma unroll
-        for (int i = 0; i < kLaT / 16; ++i)
-          umma_f16_ts(t_sc + 128 * st + 64, t_sc + 128 * st + i * 8,
-                      dv0 + st * (kLaBlk >> 4) + i * 128u, la_idesc(64, false, true), i != 0);
-        umma_commit(&s_pv[st]);
-      }
-      __syncwarp();
     }
     if (!ok) s_fail = 1;
     // every product has completed before the TMEM is given back
@@ -475,63 +493,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const long long last = limit < 2000000000LL ? 2000000000LL : limit;
     la_wait(&s_drain, 0u, last);
   } else if (warp < 10) {
-    // ---- weighted scores: thread = token, half of the columns ------------------------
-    const int i = row, x0 = rev ? 32 - i : 127 - i;
-    const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
-    for (int c = 0; FULL && c < nc; ++c) {
-      const int st = c & 1;
-      const unsigned par2 = (unsigned)(c >> 1) & 1u, t_s = t_sc + lane_off + 128 * st;
-      if (!__all_sync(0xffffffffu, la_wait(&s_sc[st], par2, limit))) {
-        s_fail = 1;
-        break;
-      }
-      tc_fence_after();
-      // two blocks of 32 columns; those beyond the diagonal block J = qd are zero
-      unsigned u[32];
-#pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const int J = 2 * hf + jj;
-        if (rev ? J >= qd : J <= qd) {  // uniform in the warp
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            unsigned r[16];
-            tmem_ld16_async(t_s + 32 * J + 16 * g, r);
-            f32x2 f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              f[e] = *reinterpret_cast<const f32x2*>(wt0 + 32 * J + 16 * g + 2 * e);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float y0, y1;
-              unpair2(mul2(pair2u(r[2 * e], r[2 * e + 1]), f[e]), y0, y1);
-              u[16 * jj + 8 * g + e] = pack_bf16(y0, y1);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[16 * jj + e] = 0u;
-        }
-      }
-      // they go to columns 0-63, where the warp of the lower half reads
-      tc_fence_before();
-      if (hf == 0) {
-        mbar_arrive(&s_rd[qd][st]);
-      } else {
-        if (!__all_sync(0xffffffffu, la_wait(&s_rd[qd][st], par2, limit))) {
-          s_fail = 1;
-          break;
-        }
-        tc_fence_after();
-      }
-      tmem_st16(t_s + 32 * hf, u);
-      tmem_st16(t_s + 32 * hf + 16, u + 16);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&s_p[st]);
-    }
-  } else if (warp < 14) {
-    // ---- outputs: thread = token ---------------------------------------------------------
+    // ---- weighted scores and outputs: thread = token, half of the columns -----------
     const int i = row;
     const long long obase = (long long)b * a.ob + (long long)h * a.oh + col0;
     const int nd = a.dv - col0 < kLaN ? a.dv - col0 : kLaN;
@@ -540,81 +502,118 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const float e_full = a.c_out * (float)la_pow(ld, rev ? kLaT - 1 - i : i + 1);
     const float e_tail =
         i < n_tail ? a.c_out * (float)la_pow(ld, rev ? n_tail - 1 - i : i + 1) : 0.0f;
+    const int x0 = rev ? 32 - i : 127 - i;
+    const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
+    if (FULL && nc > 0) mbar_arrive(&s_b);  // chunk 0 has no outputs before it
     for (int c = 0; FULL && c < nc; ++c) {
-      const int st = c & 1, n = rows(c), t = t0(c);
-      if (!__all_sync(0xffffffffu, la_wait(&s_pv[st], (unsigned)(c >> 1) & 1u, limit))) {
+      const int st = c & 1;
+      const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
+      const int n = rows(c);
+      bool ok = la_wait(&s_sc[st], par2, limit);
+      if (!__all_sync(0xffffffffu, ok)) {
         s_fail = 1;
         break;
       }
       tc_fence_after();
-      const float e = c == c_tail ? e_tail : e_full;
-      const f32x2 ee = pair2(e, e);
-      unsigned u[32];  // eight 16-byte units of this row
+      const unsigned t_s = t_sc + lane_off + 128 * st;
+      // two blocks of 32 columns; those beyond the diagonal block J = qd are zero
+      unsigned w[32];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        unsigned y[16], z[16];
-        tmem_ld16_async(t_oi + lane_off + 16 * g, y);
-        tmem_ld16_async(t_sc + lane_off + 128 * st + 64 + 16 * g, z);
-        tmem_wait_ld();
-        float x[16];
+      for (int jj = 0; jj < 2; ++jj) {
+        const int J = 2 * hf + jj;
+        if (rev ? J >= qd : J <= qd) {  // uniform in the warp
+          unsigned r[32];
+          tmem_ld16_async(t_s + 32 * J, r);
+          tmem_ld16_async(t_s + 32 * J + 16, r + 16);
+          f32x2 f[16];
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-          unpair2(fma2(ee, pair2u(y[2 * d], y[2 * d + 1]), pair2u(z[2 * d], z[2 * d + 1])),
-                  x[2 * d], x[2 * d + 1]);
-        if (f32) {
-          if (i < n) {
-            float* o = static_cast<float*>(a.o) + obase + (long long)(t + i) * a.ot + 16 * g;
+          for (int e = 0; e < 16; ++e)
+            f[e] = *reinterpret_cast<const f32x2*>(wt0 + 32 * J + 2 * e);
+          tmem_wait_ld();
 #pragma unroll
-            for (int d = 0; d < 16; d += 4)
-              if (16 * g + d < nd)
-                *reinterpret_cast<float4*>(o + d) = make_float4(x[d], x[d + 1], x[d + 2], x[d + 3]);
+          for (int e = 0; e < 16; ++e) {
+            float y0, y1;
+            unpair2(mul2(pair2u(r[2 * e], r[2 * e + 1]), f[e]), y0, y1);
+            w[16 * jj + e] = pack_bf16(y0, y1);
           }
         } else {
 #pragma unroll
-          for (int d = 0; d < 8; ++d) u[8 * g + d] = pack_bf16(x[2 * d], x[2 * d + 1]);
+          for (int e = 0; e < 16; ++e) w[16 * jj + e] = 0u;
         }
       }
+      // the weighted scores go to columns 0-63, where the warp of the lower half reads
       tc_fence_before();
-      mbar_arrive(&s_ofree);
-      if (f32) continue;
-      // 4 x 4 exchanges of units in each quad of lanes: lane j of a quad then holds units j
-      // and 4 + j of the quad's rows 0-3, and a store covers 64 bytes of 8 rows instead
-      // of 16 bytes of 32
-#pragma unroll
-      for (int d = 0; d < 32; ++d) {
-        if (d & 4) continue;
-        const unsigned got = __shfl_xor_sync(0xffffffffu, lane & 1 ? u[d] : u[d + 4], 1);
-        if (lane & 1)
-          u[d] = got;
-        else
-          u[d + 4] = got;
+      if (hf == 0) {
+        mbar_arrive(&s_rd[qd]);
+      } else {
+        ok = la_wait(&s_rd[qd], par, limit);
+        if (!__all_sync(0xffffffffu, ok)) {
+          s_fail = 1;
+          break;
+        }
+        tc_fence_after();
       }
-#pragma unroll
-      for (int d = 0; d < 32; ++d) {
-        if (d & 8) continue;
-        const unsigned got = __shfl_xor_sync(0xffffffffu, lane & 2 ? u[d] : u[d + 8], 2);
-        if (lane & 2)
-          u[d] = got;
-        else
-          u[d + 8] = got;
+      tmem_st16(t_s + 32 * hf, w);
+      tmem_st16(t_s + 32 * hf + 16, w + 16);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&s_p);
+
+      ok = la_wait(&s_pv[st], par2, limit);
+      if (!__all_sync(0xffffffffu, ok)) {
+        s_fail = 1;
+        break;
       }
-      const int i0 = i & ~3, d0 = 8 * (lane & 3);
-      __nv_bfloat16* o =
-          static_cast<__nv_bfloat16*>(a.o) + obase + (long long)(t + i0) * a.ot + d0;
+      tc_fence_after();
+      unsigned y[32];
+      tmem_ld16_async(t_oi + lane_off + 32 * hf, y);
+      tmem_ld16_async(t_s + 64 + 32 * hf, w);
+      tmem_ld16_async(t_oi + lane_off + 32 * hf + 16, y + 16);
+      tmem_ld16_async(t_s + 64 + 32 * hf + 16, w + 16);
+      const float e = c == c_tail ? e_tail : e_full;
+      const f32x2 ee = pair2(e, e);
+      tmem_wait_ld();
+      tc_fence_before();
+      if (c + 1 < nc) mbar_arrive(&s_b);  // chunk c + 1 may write the outputs
+      f32x2 x[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int d = 0; d < 16; ++d)
+        x[d] = fma2(ee, pair2u(y[2 * d], y[2 * d + 1]), pair2u(w[2 * d], w[2 * d + 1]));
+      if (staged(c)) {
+        const unsigned ob = Sm::kV + st * kLaBlk;
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (i0 + k < n && 32 * g + d0 < nd)
-            *reinterpret_cast<uint4*>(o + k * a.ot + 32 * g) =
-                make_uint4(u[16 * g + 4 * k], u[16 * g + 4 * k + 1], u[16 * g + 4 * k + 2],
-                           u[16 * g + 4 * k + 3]);
+        for (int d = 0; d < 4; ++d) {
+          unsigned u[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float x0, x1;
+            unpair2(x[4 * d + g], x0, x1);
+            u[g] = pack_bf16(x0, x1);
+          }
+          sts128(unit[d] + ob, u[0], u[1], u[2], u[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      } else if (i < n) {
+        const long long at = obase + (long long)(t0(c) + i) * a.ot + 32 * hf;
+#pragma unroll
+        for (int d = 0; d < 32; d += 4)
+          if (32 * hf + d < nd) {
+            float4 y4;
+            unpair2(x[d / 2], y4.x, y4.y);
+            unpair2(x[d / 2 + 1], y4.z, y4.w);
+            if (f32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at + d) = y4;
+            else
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at + d) =
+                  make_uint2(pack_bf16(y4.x, y4.y), pack_bf16(y4.z, y4.w));
+          }
       }
+      mbar_arrive(&s_put[st]);
     }
     if (FULL && p.zero_tail && !*(volatile int*)&s_fail) {
       const long long end = span == p.nspan - 1 ? p.L : tb + p.span;
       for (long long t = (long long)tb + len + i; t < end; t += kLaT)
-        for (int d = 0; d < nd; d += 8) {
+        for (int d = 8 * hf; d < nd; d += 16) {
           const long long at = obase + t * a.ot + d;
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           if (f32) {
@@ -660,18 +659,18 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         if (m < kLaT) la_two(la_pow(ld, m), h1, h2);
         const f32x2 hh1 = pair2(h1, h1), hh2 = pair2(h2, h2);
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          unsigned u1[8], u2[8], u3[8];
-          tmem_ld8_async(t_kv + lane_off + 32 * hf + 8 * part, u1);
-          tmem_ld8_async(t_kv + lane_off + 32 * hf + 64 + 8 * part, u2);
-          tmem_ld8_async(t_kv + lane_off + 32 * hf + 128 + 8 * part, u3);
+        for (int part = 0; part < 2; ++part) {
+          unsigned u1[16], u2[16], u3[16];
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 16 * part, u1);
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 64 + 16 * part, u2);
+          tmem_ld16_async(t_kv + lane_off + 32 * hf + 128 + 16 * part, u3);
           tmem_wait_ld();
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const f32x2 old = s[4 * part + d];
+          for (int d = 0; d < 8; ++d) {
+            const f32x2 old = s[8 * part + d];
             const f32x2 low = fma2(
                 hh2, old, add2(pair2u(u3[2 * d], u3[2 * d + 1]), pair2u(u2[2 * d], u2[2 * d + 1])));
-            s[4 * part + d] = fma2(hh1, old, add2(pair2u(u1[2 * d], u1[2 * d + 1]), low));
+            s[8 * part + d] = fma2(hh1, old, add2(pair2u(u1[2 * d], u1[2 * d + 1]), low));
           }
         }
       }
@@ -698,11 +697,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       const f32x2 ff = pair2(f, f), minus = pair2(-1.0f, -1.0f);
-      uint4 in = lds128(unit[0] + vb);
+      uint4 in[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = lds128(unit[j] + vb);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const unsigned v4[4] = {in.x, in.y, in.z, in.w};
-        if (j < 3) in = lds128(unit[j + 1] + vb);
+        const unsigned v4[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
         unsigned w1[4], w2[4], w3[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       la_walk<__nv_bfloat16, kLaN, kLaAgainThreads>(
           p, a, b, h, col0, tb, len, s_in ? s_in + sb : nullptr, sr, sc,
           s_out ? s_out + sb : nullptr, *reinterpret_cast<LaWalkSmem<kLaN>*>(dsmem));
-  } else if (warp >= 14 && s_out && row < a.dk) {
+  } else if (warp >= 10 && s_out && row < a.dk) {
 #pragma unroll
     for (int d = 0; d < 32; d += 4)
       if (cs0 + d < a.dv) {
