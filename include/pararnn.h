@@ -455,8 +455,8 @@ typedef struct {
 } pararnn_linattn_t;
 
 /* Workspace bytes of pararnn_scan_linattn (backward = 0) or its backward pass
- * (backward = 1) for these shapes; strides and scale do not matter.  0 on bad
- * sizes. */
+ * (backward = 1) for these shapes; strides and scale do not matter.  256 where the
+ * call needs none (ws may then be NULL), 0 on bad sizes. */
 size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* desc, int32_t backward);
 
 /* The scan over a prompt.
@@ -515,7 +515,8 @@ pararnn_status_t pararnn_layer_norm(const void* x, pararnn_dtype_t x_dtype, int6
                                     pararnn_dtype_t y_dtype, float* mean, float* rstd, int64_t M,
                                     int64_t D, float eps, void* stream);
 
-/* Workspace bytes of the layer norm's backward pass.  0 on bad sizes. */
+/* Workspace bytes of the layer norm's backward pass: 256 where it needs none (ws
+ * may then be NULL), 0 on bad sizes. */
 size_t pararnn_layer_norm_workspace_size(int64_t M, int64_t D);
 
 /* Its gradients: with g = dy weight and xh = (x - mean) rstd,

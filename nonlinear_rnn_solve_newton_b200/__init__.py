@@ -30,6 +30,7 @@ reused between calls on the same thread, device and stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -99,6 +100,8 @@ class _LinAttn(ctypes.Structure):
                 ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
                 ("do_stride", ctypes.c_int64 * 3)]
 
+
+_Stride3 = ctypes.c_int64 * 3
 
 INFO_BYTES = ctypes.sizeof(_Info)
 
@@ -232,7 +235,7 @@ def workspace_size(op: int, B: int, L: int, D: int, max_iters: int = 0, opts: Op
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check_dev(name, t, dtype, shape):
@@ -270,8 +273,14 @@ def _one_device(**named):
     return dev
 
 
+_same_device = contextlib.nullcontext()
+
+
 def _device_guard(dev):
-    """Makes `dev` the current device for the duration of one library call."""
+    """Makes `dev` the current device for the duration of one library call (nothing to
+    do where it already is)."""
+    if torch.cuda.current_device() == dev.index:
+        return _same_device
     return torch.cuda.device(dev)
 
 
@@ -865,21 +874,24 @@ def _stream_tensor(name, t, dtype, shape, unit):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    strides = []
-    dense = t.shape[-1]
-    if t.stride(-1) != 1 and t.numel() > 0:
+    sizes, strides = t.shape, list(t.stride())
+    if sizes != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(sizes)}")
+    if strides[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        strides.append(st if n > 1 else dense)
-        dense *= max(n, 1)
-        if unit > 1 and n > 1 and t.numel() > 0 and (st <= 0 or st % unit):
+    dense = sizes[-1]
+    for i in range(len(strides) - 2, -1, -1):
+        n = sizes[i]
+        if n <= 1:
+            strides[i] = dense
+        elif unit > 1 and (strides[i] <= 0 or strides[i] % unit) and t.numel() > 0:
             raise ValueError(f"{name}: strides must be positive multiples of {unit} elements, "
                              f"got {tuple(t.stride())}")
+        else:
+            dense *= n
     if unit > 1 and t.data_ptr() % (unit * t.element_size()):
         raise ValueError(f"{name} must start on a {unit * t.element_size()}-byte boundary")
-    return strides[::-1]
+    return strides[:-1]
 
 
 def _linattn_shapes(q, k, v, log_decay, scale, dtype, unit, tokens):
@@ -897,18 +909,23 @@ def _linattn_shapes(q, k, v, log_decay, scale, dtype, unit, tokens):
                          "of log_decay")
     if Dk % 8 or Dv % 8 or not 8 <= Dk <= 128 or not 8 <= Dv <= 128:
         raise ValueError(f"head sizes must be multiples of 8 from 8 to 128, got {Dk} and {Dv}")
-    d = _LinAttn(B=lead[0], L=lead[1] if tokens else 1, H=H, Hq=Hq, Hk=Hk, Hv=Hv, Dk=Dk, Dv=Dv,
-                 scale=float(scale))
-    for name, t, h, n in (("q", q, Hq, Dk), ("k", k, Hk, Dk), ("v", v, Hv, Dv)):
-        st = _stream_tensor(name, t, dtype, lead + (h, n), unit)
-        getattr(d, name + "_stride")[:] = st if tokens else [st[0], 0, st[1]]
+    qs = _stream_tensor("q", q, dtype, lead + (Hq, Dk), unit)
+    ks = _stream_tensor("k", k, dtype, lead + (Hk, Dk), unit)
+    vs = _stream_tensor("v", v, dtype, lead + (Hv, Dv), unit)
+    if not tokens:  # the token's stride is not used
+        for st in (qs, ks, vs):
+            st.insert(1, 0)
     _check_dev("log_decay", log_decay, torch.float32, (H,))
-    return d
+    return _LinAttn(lead[0], lead[1] if tokens else 1, H, Hq, Hk, Hv, Dk, Dv, scale, 0,
+                    _Stride3(*qs), _Stride3(*ks), _Stride3(*vs))
 
 
 def _call_buffer(nbytes, device, stream):
-    """Workspace of one call, from torch's allocator for the stream it runs on.
-    Taken anew each call, so that captured graphs keep workspaces of their own."""
+    """Workspace of one call, from torch's allocator for the stream it runs on (None
+    where the call needs none: the library then says 256).  Taken anew each call,
+    so that captured graphs keep workspaces of their own."""
+    if nbytes <= 256:
+        return None
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
@@ -948,11 +965,12 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     _check_dev("status", status, torch.int32, (1,))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s0=s0, lengths=lengths, out=out,
                       state_out=state_out, status=status)
-    ws = _call_buffer(lib.pararnn_linattn_workspace_size(ctypes.byref(d), 0), dev, stream)
+    nws = lib.pararnn_linattn_workspace_size(ctypes.byref(d), 0)
+    ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
         st = lib.pararnn_scan_linattn(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
                                       _ptr(s0), _ptr(lengths), _ptr(out), _ptr(state_out),
-                                      _ptr(ws), ws.numel(), _ptr(status),
+                                      _ptr(ws), nws, _ptr(status),
                                       ctypes.byref(opts) if opts is not None else None,
                                       _stream_handle(stream, dev))
     _raise(st, "pararnn_scan_linattn")
@@ -986,12 +1004,13 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     _check_dev("status", status, torch.int32, (1,))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
                       dq=dq, dk=dk, dv=dv, ds0=ds0, status=status)
-    ws = _call_buffer(lib.pararnn_linattn_workspace_size(ctypes.byref(d), 1), dev, stream)
+    nws = lib.pararnn_linattn_workspace_size(ctypes.byref(d), 1)
+    ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
         st = lib.pararnn_scan_linattn_backward(
             ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(s0), _ptr(do),
             _ptr(ds), _ptr(lengths), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ds0), _ptr(ws),
-            ws.numel(), _ptr(status), ctypes.byref(opts) if opts is not None else None,
+            nws, _ptr(status), ctypes.byref(opts) if opts is not None else None,
             _stream_handle(stream, dev))
     _raise(st, "pararnn_scan_linattn_backward")
     return dq, dk, dv, ds0
@@ -1115,11 +1134,12 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     _check_dev("dbias", db, torch.float32, (D,))
     dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dw,
                       dbias=db)
-    ws = _call_buffer(lib.pararnn_layer_norm_workspace_size(M, D), dev, stream)
+    nws = lib.pararnn_layer_norm_workspace_size(M, D)
+    ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
         st = lib.pararnn_layer_norm_backward(_ptr(dy), ty, sdy, _ptr(x), tx, sx, _ptr(weight),
                                              _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
-                                             _ptr(db), M, D, _ptr(ws), ws.numel(),
+                                             _ptr(db), M, D, _ptr(ws), nws,
                                              _stream_handle(stream, dev))
     _raise(st, "pararnn_layer_norm_backward")
     return dx, dw, db

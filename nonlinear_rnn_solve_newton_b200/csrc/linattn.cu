@@ -17,7 +17,7 @@ namespace {
 
 bool la_aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-size_t la_round(size_t n) { return (n + 255) / 256 * 256; }
+size_t la_round(size_t n) { return (n + 511) / 512 * 512; }  // more than kLaNoWs
 
 bool la_sizes_ok(const pararnn_linattn_t* d) {
   if (!d || d->B < 0 || d->L < 0 || d->H <= 0 || d->Hq <= 0 || d->Hk <= 0 || d->Hv <= 0)
@@ -191,6 +191,8 @@ pararnn_status_t la_launch(LaParams& lp, const LaPlan& pl, float* span_ws,
 
 // Workspace: fp32 per-head gradients of the streams whose heads are shared, and
 // the spans' states of every pass.
+constexpr size_t kLaNoWs = 256;  // what the size says where a call needs none
+
 struct LaWs {
   size_t dq, dk, dv, span, total;
 };
@@ -209,7 +211,7 @@ LaWs la_ws(const pararnn_linattn_t* d, bool backward, const LaPlan& pl) {
   w.span = at;
   if (pl.nspan > 1)
     at += la_round((size_t)(backward ? 3 : 1) * d->B * d->H * pl.nspan * d->Dk * d->Dv * 4);
-  w.total = at ? at : 256;
+  w.total = at ? at : kLaNoWs;
   return w;
 }
 
@@ -262,7 +264,8 @@ extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, con
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
   const LaPlan pl = la_plan(d, false, opts);
   const LaWs w = la_ws(d, false, pl);
-  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
+  if (w.total > kLaNoWs && (!ws || ws_bytes < w.total || !la_aligned(ws, 256)))
+    return PARARNN_ERR_WORKSPACE;
   if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
     return PARARNN_ERR_CUDA;
   if (d->B == 0) return PARARNN_OK;
@@ -318,7 +321,8 @@ extern "C" pararnn_status_t pararnn_scan_linattn_backward(
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
   const LaPlan pl = la_plan(d, true, opts);
   const LaWs w = la_ws(d, true, pl);
-  if (!ws || ws_bytes < w.total || !la_aligned(ws, 256)) return PARARNN_ERR_WORKSPACE;
+  if (w.total > kLaNoWs && (!ws || ws_bytes < w.total || !la_aligned(ws, 256)))
+    return PARARNN_ERR_WORKSPACE;
   if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), st) != cudaSuccess)
     return PARARNN_ERR_CUDA;
   if (d->B == 0) return PARARNN_OK;

@@ -11,10 +11,10 @@
 namespace pararnn {
 namespace {
 
-constexpr int kNormParts = 148;
+constexpr int kNormSms = 148;
 
 bool norm_sizes_ok(int64_t M, int64_t D) {
-  return M >= 0 && D > 0 && D < (1LL << 31) && M < (1LL << 31) * 4 && M < (1LL << 62) / D;
+  return M >= 0 && D > 0 && D < (1LL << 31) && M < (1LL << 31) && M < (1LL << 62) / D;
 }
 
 bool norm_aligned(const void* p, pararnn_dtype_t t) {
@@ -23,18 +23,119 @@ bool norm_aligned(const void* p, pararnn_dtype_t t) {
 
 bool norm_dtype_ok(pararnn_dtype_t t) { return t == PARARNN_F32 || t == PARARNN_BF16; }
 
-int norm_parts(int64_t M) { return (int)(M < 1 ? 1 : (M < kNormParts ? M : kNormParts)); }
+// Most CTAs of the backward pass: 8 a SM of small ones, and no more partial sums than
+// 8 CTAs of 1024 columns a SM would write (at M = 16384, D = 4096 they are 4% of the
+// traffic).
+int norm_max_parts(int64_t D) {
+  const int64_t n = (int64_t)kNormSms * 8 * 1024 / D;
+  return (int)(n > kNormSms * 8 ? kNormSms * 8 : (n < kNormSms ? kNormSms : n));
+}
 
 size_t norm_ws(int64_t M, int64_t D) {
-  return ((size_t)2 * norm_parts(M) * D * 4 + 255) / 256 * 256;
+  const int64_t most = norm_max_parts(D);
+  if (M <= 1) return 256;  // needs none
+  return ((size_t)2 * (M < most ? M : most) * D * 4 + 255) / 256 * 256 + 256;
+}
+
+// How a row is held.  Whole warps hold up to kWarpGroups groups a lane, a CTA the rest;
+// rows that 512 threads cannot hold are read more than once.
+struct NormShape {
+  bool vec, cta, fits;
+  int tpr, groups;  // threads of a row, groups a thread
+};
+
+bool norm_vec(const void* p, pararnn_dtype_t t, int64_t stride, int64_t M) {
+  const int unit = t == PARARNN_F32 ? 4 : 8;
+  return ((uintptr_t)p % 16) == 0 && (M <= 1 || stride % unit == 0);
+}
+
+NormShape norm_shape(bool vec, int64_t D, int warp_groups, int cta_groups, int most_groups) {
+  NormShape s = {vec, false, true, 1, warp_groups};
+  const int64_t n = vec ? D / 8 : D;  // groups of a row
+  if (n <= 32 * warp_groups) {
+    while ((int64_t)s.tpr * warp_groups < n) s.tpr *= 2;
+    while (s.groups > 1 && (int64_t)s.tpr * (s.groups / 2) >= n) s.groups /= 2;
+    return s;
+  }
+  s.cta = true;
+  s.groups = cta_groups;
+  if (n > 512LL * cta_groups) s.groups = most_groups;
+  s.tpr = 64;
+  while (s.tpr < 512 && (int64_t)s.tpr * s.groups < n) s.tpr *= 2;
+  s.fits = (int64_t)s.tpr * s.groups >= n;
+  return s;
+}
+
+template <typename TX, typename TY, int VEC, int G>
+void norm_fwd_go(NormParams& np, const NormShape& sh, cudaStream_t st) {
+  np.tpr = sh.tpr;
+  if (sh.cta) {
+    pararnn_norm_kernel<TX, TY, VEC, G, true><<<(unsigned)np.M, sh.tpr, 0, st>>>(np);
+  } else {
+    const long long rows = (long long)(kNormThreads / 32) * (32 / sh.tpr);
+    pararnn_norm_kernel<TX, TY, VEC, G, false>
+        <<<(unsigned)((np.M + rows - 1) / rows), kNormThreads, 0, st>>>(np);
+  }
 }
 
 template <typename TX, typename TY>
-void norm_bwd_launch(const NormParams& np, cudaStream_t st) {
-  pararnn_norm_dx_kernel<TX, TY><<<(unsigned)((np.M + 7) / 8), 256, 0, st>>>(np);
-  pararnn_norm_dw_kernel<TX, TY><<<dim3((unsigned)((np.D + 127) / 128), (unsigned)np.nparts), 128,
-                                   0, st>>>(np);
-  pararnn_norm_join_kernel<<<(unsigned)((np.D + 127) / 128), 128, 0, st>>>(np);
+void norm_fwd(NormParams& np, bool vec, cudaStream_t st) {
+  // up to 4 groups of 8 a lane (128 bytes of fp32), 16 single elements
+  const NormShape sh = vec ? norm_shape(true, np.D, 4, 4, 4) : norm_shape(false, np.D, 16, 16, 16);
+  if (!sh.fits) {
+    pararnn_norm_long_kernel<TX, TY><<<(unsigned)np.M, 1024, 0, st>>>(np);
+  } else if (vec) {
+    if (sh.groups == 4)
+      norm_fwd_go<TX, TY, 8, 4>(np, sh, st);
+    else if (sh.groups == 2)
+      norm_fwd_go<TX, TY, 8, 2>(np, sh, st);
+    else
+      norm_fwd_go<TX, TY, 8, 1>(np, sh, st);
+  } else {
+    norm_fwd_go<TX, TY, 1, 16>(np, sh, st);
+  }
+}
+
+template <typename TX, typename TY, int VEC, int G, int R>
+void norm_bwd_go(NormParams& np, const NormShape& sh, cudaStream_t st) {
+  np.tpr = sh.tpr;
+  const long long rows = sh.cta ? 1 : (long long)(kNormThreads / 32) * (32 / sh.tpr);
+  // enough CTAs to fill the SMs (512 threads of a CTA-wide row, or two 8-warp CTAs), each
+  // with R rows at a time
+  long long most = sh.cta ? (long long)kNormSms * (512 / sh.tpr) : 2LL * kNormSms;
+  if (most > norm_max_parts(np.D)) most = norm_max_parts(np.D);
+  const long long want = (np.M + rows - 1) / rows;
+  np.nparts = (int)(want < most ? want : most);
+  if (sh.cta)
+    pararnn_norm_bwd_kernel<TX, TY, VEC, G, R, true><<<np.nparts, sh.tpr, 0, st>>>(np);
+  else
+    pararnn_norm_bwd_kernel<TX, TY, VEC, G, R, false>
+        <<<np.nparts, kNormThreads, 8 * (size_t)np.D, st>>>(np);
+}
+
+template <typename TX, typename TY>
+void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
+  const NormShape sh = vec ? norm_shape(true, np.D, 2, 2, 4) : norm_shape(false, np.D, 16, 16, 16);
+  if (!sh.fits) {
+    np.nparts = (int)(np.M < kNormSms ? np.M : kNormSms);
+    pararnn_norm_long_dx_kernel<TX, TY><<<(unsigned)np.M, 1024, 0, st>>>(np);
+    pararnn_norm_long_dw_kernel<TX, TY>
+        <<<dim3((unsigned)((np.D + 127) / 128), (unsigned)np.nparts), 128, 0, st>>>(np);
+    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 256, 0, st>>>(np);
+    return;
+  }
+  if (vec) {
+    if (sh.groups == 4)
+      norm_bwd_go<TX, TY, 8, 4, 1>(np, sh, st);
+    else if (sh.groups == 2)
+      norm_bwd_go<TX, TY, 8, 2, 2>(np, sh, st);
+    else
+      norm_bwd_go<TX, TY, 8, 1, 4>(np, sh, st);
+  } else {
+    norm_bwd_go<TX, TY, 1, 16, 1>(np, sh, st);
+  }
+  if (np.nparts > 1)
+    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 256, 0, st>>>(np);
 }
 
 }  // namespace
@@ -69,17 +170,19 @@ extern "C" pararnn_status_t pararnn_layer_norm(const void* x, pararnn_dtype_t x_
   np.sx = x_stride;
   np.eps = eps;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((M + 7) / 8);
+  const bool vec = D % 8 == 0 && norm_vec(x, x_dtype, x_stride, M) &&
+                   norm_vec(y, y_dtype, D, M) && norm_vec(weight, PARARNN_F32, 0, 0) &&
+                   norm_vec(bias, PARARNN_F32, 0, 0);
   if (x_dtype == PARARNN_F32) {
     if (y_dtype == PARARNN_F32)
-      pararnn_norm_kernel<float, float><<<grid, 256, 0, st>>>(np);
+      norm_fwd<float, float>(np, vec, st);
     else
-      pararnn_norm_kernel<float, __nv_bfloat16><<<grid, 256, 0, st>>>(np);
+      norm_fwd<float, __nv_bfloat16>(np, vec, st);
   } else {
     if (y_dtype == PARARNN_F32)
-      pararnn_norm_kernel<__nv_bfloat16, float><<<grid, 256, 0, st>>>(np);
+      norm_fwd<__nv_bfloat16, float>(np, vec, st);
     else
-      pararnn_norm_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(np);
+      norm_fwd<__nv_bfloat16, __nv_bfloat16>(np, vec, st);
   }
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }
@@ -111,7 +214,9 @@ extern "C" pararnn_status_t pararnn_layer_norm_backward(
       !norm_aligned(weight, PARARNN_F32) || !norm_aligned(mean, PARARNN_F32) ||
       !norm_aligned(rstd, PARARNN_F32))
     return PARARNN_ERR_INVALID_ARGUMENT;
-  if (!ws || ws_bytes < norm_ws(M, D) || ((uintptr_t)ws % 256) != 0) return PARARNN_ERR_WORKSPACE;
+  // one row, one partial sum: it is the result
+  if (M > 1 && (!ws || ws_bytes < norm_ws(M, D) || ((uintptr_t)ws % 256) != 0))
+    return PARARNN_ERR_WORKSPACE;
   NormParams np = {};
   np.x = x;
   np.dy = dy;
@@ -126,17 +231,19 @@ extern "C" pararnn_status_t pararnn_layer_norm_backward(
   np.D = (int)D;
   np.sx = x_stride;
   np.sdy = dy_stride;
-  np.nparts = norm_parts(M);
+  const bool vec = D % 8 == 0 && norm_vec(x, x_dtype, x_stride, M) &&
+                   norm_vec(dy, dy_dtype, dy_stride, M) && norm_vec(dx, x_dtype, D, M) &&
+                   norm_vec(weight, PARARNN_F32, 0, 0);
   if (x_dtype == PARARNN_F32) {
     if (dy_dtype == PARARNN_F32)
-      norm_bwd_launch<float, float>(np, st);
+      norm_bwd<float, float>(np, vec, st);
     else
-      norm_bwd_launch<float, __nv_bfloat16>(np, st);
+      norm_bwd<float, __nv_bfloat16>(np, vec, st);
   } else {
     if (dy_dtype == PARARNN_F32)
-      norm_bwd_launch<__nv_bfloat16, float>(np, st);
+      norm_bwd<__nv_bfloat16, float>(np, vec, st);
     else
-      norm_bwd_launch<__nv_bfloat16, __nv_bfloat16>(np, st);
+      norm_bwd<__nv_bfloat16, __nv_bfloat16>(np, vec, st);
   }
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }

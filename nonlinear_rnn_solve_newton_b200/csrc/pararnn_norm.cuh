@@ -5,7 +5,18 @@
 //   g = dy w,  xh = (x - mean) rstd
 //   dx = rstd (g - mean(g) - xh mean(g xh)),  dw = sum dy xh,  db = sum dy
 //
-// All sums are fp32; the variance is the two-pass one (mean first).
+// Bound by memory: a row is read once into registers, its sums are taken there
+// (the variance about the mean), and its results are written.  All sums are fp32.
+//
+// A row is held by `tpr` threads, thread l with the groups l, l + tpr, ... of VEC
+// elements: lanes of a warp (tpr <= 32, 32 / tpr rows a warp), or a whole CTA.
+// VEC = 8 moves 16 bytes at a time and needs 16-byte rows; VEC = 1 takes any size
+// and alignment.
+//
+// Backward: CTAs stay and take rows in turn; a thread adds up dw and db of its own
+// columns in registers over all its rows, the CTA writes one partial sum per
+// column, and a second kernel joins the CTAs' sums in a fixed order (the same bits
+// every call).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,104 +37,401 @@ struct NormParams {
   float* dw;        // [D]
   float* db;        // [D]
   long long M, sx, sdy;
-  int D, nparts;
+  int D, nparts, tpr;
   float eps;
 };
 
-__device__ __forceinline__ float norm_load(const float* p) { return *p; }
-__device__ __forceinline__ float norm_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void norm_store(float* p, float v) { *p = v; }
-__device__ __forceinline__ void norm_store(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
-}
+constexpr int kNormThreads = 256;  // of a CTA whose warps hold whole rows
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int VEC> __device__ __forceinline__ void norm_load(const float* p, float* v) {
+  if constexpr (VEC == 8) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = __ldcs(p);
+  }
+}
+template <int VEC> __device__ __forceinline__ void norm_load(const __nv_bfloat16* p, float* v) {
+  if constexpr (VEC == 8) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+    const unsigned u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-  return v;
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  } else {
+    v[0] = __bfloat162float(*p);
+  }
+}
+// weights: read again by every row, so they stay in the caches
+template <int VEC> __device__ __forceinline__ void norm_weight(const float* p, int at, float none,
+                                                               float* v) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] = none;
+  if (!p) return;
+  if constexpr (VEC == 8) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + at));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p + at) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = __ldg(p + at);
+  }
+}
+template <int VEC> __device__ __forceinline__ void norm_store(float* p, const float* v) {
+  if constexpr (VEC == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *p = v[0];
+  }
+}
+template <int VEC> __device__ __forceinline__ void norm_store(__nv_bfloat16* p, const float* v) {
+  if constexpr (VEC == 8) {
+    unsigned u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const unsigned*>(&t);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    *p = __float2bfloat16_rn(v[0]);
+  }
 }
 
-// One warp per row.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(256) pararnn_norm_kernel(const __grid_constant__ NormParams p) {
-  const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
+// Sums of N values over a row's threads, in every one of them.  In a CTA the
+// shared array is used in turns (turn = 0, 1, 0, ...), so one barrier does.
+template <int N, bool CTA>
+__device__ __forceinline__ void norm_sum(float* v, int tpr, float (*sm)[2][N], int turn) {
+  const int width = CTA ? 32 : tpr;
+  for (int s = width >> 1; s > 0; s >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], s);
+  }
+  if constexpr (CTA) {
+    const int warp = threadIdx.x >> 5, nw = tpr >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sm[warp][turn][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    for (int w = 0; w < nw; ++w) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += sm[w][turn][i];
+    }
+  }
+}
+
+template <typename TX, typename TY, int VEC, int G, bool CTA>
+__global__ void __launch_bounds__(CTA ? 512 : kNormThreads)
+    pararnn_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[CTA ? 16 : 1][2][1];
   const int lane = threadIdx.x & 31;
-  if (row >= p.M) return;
+  const int l = CTA ? (int)threadIdx.x : lane % p.tpr;
+  const long long row = CTA ? (long long)blockIdx.x
+                            : (blockIdx.x * (long long)(kNormThreads / 32) + (threadIdx.x >> 5)) *
+                                      (32 / p.tpr) + lane / p.tpr;
+  const bool live = row < p.M;  // the same for every thread of a row
+  const int ng = p.D / VEC;
   const TX* x = static_cast<const TX*>(p.x) + row * p.sx;
+  float v[G][VEC], s[1] = {0.0f};
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int at = l + g * p.tpr;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[g][i] = 0.0f;
+    if (live && at < ng) norm_load<VEC>(x + at * VEC, v[g]);
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[0] += v[g][i];
+  }
+  norm_sum<1, CTA>(s, p.tpr, sm, 0);
+  const float mean = s[0] / (float)p.D;
+  s[0] = 0.0f;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (l + g * p.tpr < ng) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        v[g][i] -= mean;
+        s[0] = fmaf(v[g][i], v[g][i], s[0]);
+      }
+    }
+  }
+  norm_sum<1, CTA>(s, p.tpr, sm, 1);
+  const float rstd = 1.0f / sqrtf(s[0] / (float)p.D + p.eps);
+  if (!live) return;
   TY* y = static_cast<TY*>(p.y) + row * p.D;
-  float s = 0.0f;
-  for (int d = lane; d < p.D; d += 32) s += norm_load(x + d);
-  const float mean = warp_sum(s) / (float)p.D;
-  s = 0.0f;
-  for (int d = lane; d < p.D; d += 32) {
-    const float c = norm_load(x + d) - mean;
-    s = fmaf(c, c, s);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int at = (l + g * p.tpr) * VEC;
+    if (at < p.D) {
+      float w[VEC], b[VEC];
+      norm_weight<VEC>(p.w, at, 1.0f, w);
+      norm_weight<VEC>(p.b, at, 0.0f, b);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[g][i] = fmaf(v[g][i] * rstd, w[i], b[i]);
+      norm_store<VEC>(y + at, v[g]);
+    }
   }
-  const float rstd = 1.0f / sqrtf(warp_sum(s) / (float)p.D + p.eps);
-  for (int d = lane; d < p.D; d += 32) {
-    const float xh = (norm_load(x + d) - mean) * rstd;
-    norm_store(y + d, fmaf(xh, p.w ? p.w[d] : 1.0f, p.b ? p.b[d] : 0.0f));
-  }
-  if (lane == 0) {
+  if (l == 0) {
     p.mean[row] = mean;
     p.rstd[row] = rstd;
   }
 }
 
-// dx, one warp per row.
+// R rows at a time, so that enough loads are in flight: G R groups a thread.
+template <typename TX, typename TY, int VEC, int G, int R, bool CTA>
+__global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
+    pararnn_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[CTA ? 16 : 1][2][2 * R];
+  extern __shared__ float cols[];  // without CTA: [2][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int l = CTA ? (int)threadIdx.x : lane % p.tpr;
+  const int rpw = CTA ? 1 : 32 / p.tpr;                       // rows side by side in a warp
+  const int rpc = CTA ? 1 : rpw * (kNormThreads / 32);        // and in a CTA
+  const long long stride = (long long)gridDim.x * rpc;        // from one row of a thread to the next
+  const int ng = p.D / VEC;
+  const float inv = 1.0f / (float)p.D;
+  float aw[G][VEC], ab[G][VEC];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) aw[g][i] = ab[g][i] = 0.0f;
+  }
+  int turn = 0;
+  const long long lead = blockIdx.x * (long long)rpc + (CTA ? 0 : warp * rpw);  // uniform in a warp
+  for (long long r0 = lead; r0 < p.M; r0 += R * stride) {
+    float x[R][G][VEC], dy[R][G][VEC], rstd[R], s[2 * R];
+    const long long row0 = r0 + (CTA ? 0 : lane / p.tpr);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r * stride;
+      const bool live = row < p.M;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int at = l + g * p.tpr;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[r][g][i] = dy[r][g][i] = 0.0f;
+        if (live && at < ng) {
+          norm_load<VEC>(static_cast<const TX*>(p.x) + row * p.sx + at * VEC, x[r][g]);
+          norm_load<VEC>(static_cast<const TY*>(p.dy) + row * p.sdy + at * VEC, dy[r][g]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r * stride;
+      const bool live = row < p.M;
+      const float mean = live ? __ldg(p.mean + row) : 0.0f;
+      rstd[r] = live ? __ldg(p.rstd + row) : 0.0f;
+      s[2 * r] = s[2 * r + 1] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int at = l + g * p.tpr;
+        float w[VEC];
+        norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float xh = (x[r][g][i] - mean) * rstd[r];
+          x[r][g][i] = xh;
+          aw[g][i] = fmaf(dy[r][g][i], xh, aw[g][i]);
+          ab[g][i] += dy[r][g][i];
+          dy[r][g][i] *= w[i];
+          s[2 * r] += dy[r][g][i];
+          s[2 * r + 1] = fmaf(dy[r][g][i], xh, s[2 * r + 1]);
+        }
+      }
+    }
+    norm_sum<2 * R, CTA>(s, p.tpr, sm, turn);
+    turn ^= 1;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = row0 + r * stride;
+      if (row < p.M) {
+        const float mg = s[2 * r] * inv, mgx = s[2 * r + 1] * inv;
+        TX* dx = static_cast<TX*>(p.y) + row * p.D;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int at = (l + g * p.tpr) * VEC;
+          if (at < p.D) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              x[r][g][i] = rstd[r] * (dy[r][g][i] - mg - x[r][g][i] * mgx);
+            norm_store<VEC>(dx + at, x[r][g]);
+          }
+        }
+      }
+    }
+  }
+
+  // one partial sum per column and CTA
+  float* pw = p.nparts > 1 ? p.part + (long long)blockIdx.x * p.D : p.dw;
+  float* pb = p.nparts > 1 ? p.part + (long long)(p.nparts + blockIdx.x) * p.D : p.db;
+  if constexpr (!CTA) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        for (int t = p.tpr; t < 32; t <<= 1) {
+          aw[g][i] += __shfl_xor_sync(0xffffffffu, aw[g][i], t);
+          ab[g][i] += __shfl_xor_sync(0xffffffffu, ab[g][i], t);
+        }
+    }
+    for (int w = 0; w < kNormThreads / 32; ++w) {  // the warps in turn
+      if (warp == w && lane < p.tpr) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int at = (l + g * p.tpr) * VEC;
+          if (at < p.D) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              cols[at + i] = (w ? cols[at + i] : 0.0f) + aw[g][i];
+              cols[p.D + at + i] = (w ? cols[p.D + at + i] : 0.0f) + ab[g][i];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
+      pw[d] = cols[d];
+      pb[d] = cols[p.D + d];
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int at = (l + g * p.tpr) * VEC;
+      if (at < p.D) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          pw[at + i] = aw[g][i];
+          pb[at + i] = ab[g][i];
+        }
+      }
+    }
+  }
+}
+
+// The CTAs' sums, joined in a fixed order: 32 columns x 8 slices of the parts.
+__global__ void __launch_bounds__(256) pararnn_norm_join_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[8][2][32];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
+  float sw = 0.0f, sb = 0.0f;
+  if (d < p.D) {
+#pragma unroll 4
+    for (int i = slice; i < p.nparts; i += 8) {
+      sw += p.part[(long long)i * p.D + d];
+      sb += p.part[(long long)(p.nparts + i) * p.D + d];
+    }
+  }
+  sm[slice][0][lane] = sw;
+  sm[slice][1][lane] = sb;
+  __syncthreads();
+  if (slice < 2 && d < p.D) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += sm[i][slice][lane];
+    (slice ? p.db : p.dw)[d] = s;
+  }
+}
+
+// ---- rows of any length (longer than the threads' registers hold) -------------------
+__device__ __forceinline__ float norm_block_sum(float v, float* sm) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) v += sm[w];
+  return v;
+}
+
 template <typename TX, typename TY>
-__global__ void __launch_bounds__(256)
-    pararnn_norm_dx_kernel(const __grid_constant__ NormParams p) {
-  const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= p.M) return;
+__global__ void __launch_bounds__(1024)
+    pararnn_norm_long_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[32];
+  const long long row = blockIdx.x;
+  const TX* x = static_cast<const TX*>(p.x) + row * p.sx;
+  TY* y = static_cast<TY*>(p.y) + row * p.D;
+  float s = 0.0f, v[1], w[1], b[1];
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    norm_load<1>(x + d, v);
+    s += v[0];
+  }
+  const float mean = norm_block_sum(s, sm) / (float)p.D;
+  s = 0.0f;
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    norm_load<1>(x + d, v);
+    s = fmaf(v[0] - mean, v[0] - mean, s);
+  }
+  const float rstd = 1.0f / sqrtf(norm_block_sum(s, sm) / (float)p.D + p.eps);
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    norm_load<1>(x + d, v);
+    norm_weight<1>(p.w, d, 1.0f, w);
+    norm_weight<1>(p.b, d, 0.0f, b);
+    v[0] = fmaf((v[0] - mean) * rstd, w[0], b[0]);
+    norm_store<1>(y + d, v);
+  }
+  if (threadIdx.x == 0) {
+    p.mean[row] = mean;
+    p.rstd[row] = rstd;
+  }
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(1024)
+    pararnn_norm_long_dx_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[32];
+  const long long row = blockIdx.x;
   const TX* x = static_cast<const TX*>(p.x) + row * p.sx;
   const TY* dy = static_cast<const TY*>(p.dy) + row * p.sdy;
   TX* dx = static_cast<TX*>(p.y) + row * p.D;
   const float mean = p.mean[row], rstd = p.rstd[row];
-  float sg = 0.0f, sgx = 0.0f;
-  for (int d = lane; d < p.D; d += 32) {
-    const float g = norm_load(dy + d) * (p.w ? p.w[d] : 1.0f);
-    sg += g;
-    sgx = fmaf(g, (norm_load(x + d) - mean) * rstd, sgx);
+  float sg = 0.0f, sgx = 0.0f, v[1], g[1], w[1];
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    norm_load<1>(x + d, v);
+    norm_load<1>(dy + d, g);
+    norm_weight<1>(p.w, d, 1.0f, w);
+    sg += g[0] * w[0];
+    sgx = fmaf(g[0] * w[0], (v[0] - mean) * rstd, sgx);
   }
-  const float mg = warp_sum(sg) / (float)p.D, mgx = warp_sum(sgx) / (float)p.D;
-  for (int d = lane; d < p.D; d += 32) {
-    const float g = norm_load(dy + d) * (p.w ? p.w[d] : 1.0f);
-    const float xh = (norm_load(x + d) - mean) * rstd;
-    norm_store(dx + d, rstd * (g - mg - xh * mgx));
+  const float mg = norm_block_sum(sg, sm) / (float)p.D;
+  const float mgx = norm_block_sum(sgx, sm) / (float)p.D;
+  for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+    norm_load<1>(x + d, v);
+    norm_load<1>(dy + d, g);
+    norm_weight<1>(p.w, d, 1.0f, w);
+    v[0] = rstd * (g[0] * w[0] - mg - (v[0] - mean) * rstd * mgx);
+    norm_store<1>(dx + d, v);
   }
 }
 
-// Column sums of one slice of rows: thread = column.
+// column sums of one slice of rows: thread = column
 template <typename TX, typename TY>
 __global__ void __launch_bounds__(128)
-    pararnn_norm_dw_kernel(const __grid_constant__ NormParams p) {
+    pararnn_norm_long_dw_kernel(const __grid_constant__ NormParams p) {
   const int d = blockIdx.x * 128 + threadIdx.x;
   if (d >= p.D) return;
   const long long lo = p.M * blockIdx.y / p.nparts, hi = p.M * (blockIdx.y + 1) / p.nparts;
-  float sw = 0.0f, sb = 0.0f;
+  float sw = 0.0f, sb = 0.0f, v[1], g[1];
   for (long long r = lo; r < hi; ++r) {
-    const float dy = norm_load(static_cast<const TY*>(p.dy) + r * p.sdy + d);
-    const float xh = (norm_load(static_cast<const TX*>(p.x) + r * p.sx + d) - p.mean[r]) * p.rstd[r];
-    sw = fmaf(dy, xh, sw);
-    sb += dy;
+    norm_load<1>(static_cast<const TY*>(p.dy) + r * p.sdy + d, g);
+    norm_load<1>(static_cast<const TX*>(p.x) + r * p.sx + d, v);
+    sw = fmaf(g[0], (v[0] - p.mean[r]) * p.rstd[r], sw);
+    sb += g[0];
   }
   p.part[(long long)blockIdx.y * p.D + d] = sw;
   p.part[(long long)(p.nparts + blockIdx.y) * p.D + d] = sb;
-}
-
-// The slices' sums, joined in a fixed order.
-__global__ void pararnn_norm_join_kernel(const __grid_constant__ NormParams p) {
-  const int d = blockIdx.x * blockDim.x + threadIdx.x;
-  if (d >= p.D) return;
-  float sw = 0.0f, sb = 0.0f;
-  for (int i = 0; i < p.nparts; ++i) {
-    sw += p.part[(long long)i * p.D + d];
-    sb += p.part[(long long)(p.nparts + i) * p.D + d];
-  }
-  p.dw[d] = sw;
-  p.db[d] = sb;
 }
 
 }  // namespace pararnn

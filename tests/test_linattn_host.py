@@ -104,7 +104,10 @@ def test_linattn_abi_validation():
         for st in ([0, 128, 24], [1024, -8, 24], [1024, 128, 12]):
             assert scan(_desc(**{name + "_stride": st})) == 1, (name, st)
     assert back(_desc(do_stride=[1024, 128, 20])) == 1
-    assert scan(d, w=None) == 6 and scan(d, nb=16) == 6 and scan(d, w=vp(4100)) == 6
+    long = _desc(L=4096)                      # cut into spans: their states need room
+    need = lib.pararnn_linattn_workspace_size(ctypes.byref(long), 0)
+    assert need > 256
+    assert scan(long, w=None) == 6 and scan(long, nb=need - 1) == 6 and scan(long, w=vp(4100)) == 6
     for name in ("q", "k", "v", "g", "do", "dq", "dk", "dv"):
         assert back(d, **{name: None}) == 1, name
     assert back(d, do=odd) == 1 and back(d, dq=odd) == 1 and back(d, ds0=odd) == 1
