@@ -128,9 +128,9 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
     if (sh.groups == 4)
       norm_bwd_go<TX, TY, 8, 4, 1>(np, sh, st);
     else if (sh.groups == 2)
-      norm_bwd_go<TX, TY, 8, 2, 2>(np, sh, st);
+      norm_bwd_go<TX, TY, 8, 2, 1>(np, sh, st);
     else
-      norm_bwd_go<TX, TY, 8, 1, 4>(np, sh, st);
+      norm_bwd_go<TX, TY, 8, 1, 2>(np, sh, st);
   } else {
     norm_bwd_go<TX, TY, 1, 16, 1>(np, sh, st);
   }

@@ -188,7 +188,46 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads)
   }
 }
 
-// R rows at a time, so that enough loads are in flight: G R groups a thread.
+// A group as it lies in memory.
+template <typename T, int VEC> struct NormRaw;
+template <> struct NormRaw<float, 8> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <> struct NormRaw<__nv_bfloat16, 8> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float* v) const {
+    const unsigned u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <typename T> struct NormRaw<T, 1> {
+  float a;
+  __device__ __forceinline__ void load(const T* p) { norm_load<1>(p, &a); }
+  __device__ __forceinline__ void zero() { a = 0.0f; }
+  __device__ __forceinline__ void get(float* v) const { v[0] = a; }
+};
+
+// R rows at a time, and the next R on their way while these are worked on: what is in
+// flight covers the latency of HBM.  The rows stay as they lie in memory and are
+// unpacked twice (for the sums, and for dx), which costs fewer registers than keeping
+// them as fp32.
 template <typename TX, typename TY, int VEC, int G, int R, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
     pararnn_norm_bwd_kernel(const __grid_constant__ NormParams p) {
@@ -196,58 +235,74 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
   extern __shared__ float cols[];  // without CTA: [2][D]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = CTA ? (int)threadIdx.x : lane % p.tpr;
-  const int rpw = CTA ? 1 : 32 / p.tpr;                       // rows side by side in a warp
-  const int rpc = CTA ? 1 : rpw * (kNormThreads / 32);        // and in a CTA
-  const long long stride = (long long)gridDim.x * rpc;        // from one row of a thread to the next
+  const int rpw = CTA ? 1 : 32 / p.tpr;                  // rows side by side in a warp
+  const int rpc = CTA ? 1 : rpw * (kNormThreads / 32);   // and in a CTA
+  const long long stride = (long long)gridDim.x * rpc;   // from one row of a thread to the next
   const int ng = p.D / VEC;
   const float inv = 1.0f / (float)p.D;
-  float aw[G][VEC], ab[G][VEC];
+  constexpr bool KEEP = G * VEC <= 16;  // the weights stay in registers
+  float aw[G][VEC], ab[G][VEC], w[KEEP ? G : 1][VEC];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
+    if constexpr (KEEP) {
+      const int at = l + g * p.tpr;
+      norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, w[g]);
+    }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) aw[g][i] = ab[g][i] = 0.0f;
   }
-  int turn = 0;
-  const long long lead = blockIdx.x * (long long)rpc + (CTA ? 0 : warp * rpw);  // uniform in a warp
-  for (long long r0 = lead; r0 < p.M; r0 += R * stride) {
-    float x[R][G][VEC], dy[R][G][VEC], rstd[R], s[2 * R];
-    const long long row0 = r0 + (CTA ? 0 : lane / p.tpr);
+  struct Rows {
+    NormRaw<TX, VEC> x[R][G];
+    NormRaw<TY, VEC> dy[R][G];
+    float mean[R], rstd[R];
+  };
+  const auto fetch = [&](Rows& q, long long row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r * stride;
       const bool live = row < p.M;
+      q.mean[r] = live ? __ldg(p.mean + row) : 0.0f;
+      q.rstd[r] = live ? __ldg(p.rstd + row) : 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int at = l + g * p.tpr;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[r][g][i] = dy[r][g][i] = 0.0f;
+        q.x[r][g].zero();
+        q.dy[r][g].zero();
         if (live && at < ng) {
-          norm_load<VEC>(static_cast<const TX*>(p.x) + row * p.sx + at * VEC, x[r][g]);
-          norm_load<VEC>(static_cast<const TY*>(p.dy) + row * p.sdy + at * VEC, dy[r][g]);
+          q.x[r][g].load(static_cast<const TX*>(p.x) + row * p.sx + at * VEC);
+          q.dy[r][g].load(static_cast<const TY*>(p.dy) + row * p.sdy + at * VEC);
         }
       }
     }
+  };
+  int turn = 0;
+  const long long lead = blockIdx.x * (long long)rpc + (CTA ? 0 : warp * rpw);  // uniform in a warp
+  const long long own = CTA ? 0 : lane / p.tpr;
+  constexpr bool AHEAD = G * VEC <= 16;  // (four groups a thread leave no room for a second set)
+  Rows cur, nxt;
+  if (AHEAD) fetch(cur, lead + own);
+  for (long long r0 = lead; r0 < p.M; r0 += R * stride) {
+    const long long row0 = r0 + own;
+    fetch(AHEAD ? nxt : cur, AHEAD ? row0 + R * stride : row0);
+    float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const long long row = row0 + r * stride;
-      const bool live = row < p.M;
-      const float mean = live ? __ldg(p.mean + row) : 0.0f;
-      rstd[r] = live ? __ldg(p.rstd + row) : 0.0f;
       s[2 * r] = s[2 * r + 1] = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        float x[VEC], dy[VEC], wr[VEC];
+        cur.x[r][g].get(x);
+        cur.dy[r][g].get(dy);
         const int at = l + g * p.tpr;
-        float w[VEC];
-        norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, w);
+        if constexpr (!KEEP) norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, wr);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float xh = (x[r][g][i] - mean) * rstd[r];
-          x[r][g][i] = xh;
-          aw[g][i] = fmaf(dy[r][g][i], xh, aw[g][i]);
-          ab[g][i] += dy[r][g][i];
-          dy[r][g][i] *= w[i];
-          s[2 * r] += dy[r][g][i];
-          s[2 * r + 1] = fmaf(dy[r][g][i], xh, s[2 * r + 1]);
+          const float xh = (x[i] - cur.mean[r]) * cur.rstd[r];
+          const float dyw = dy[i] * (KEEP ? w[KEEP ? g : 0][i] : wr[i]);
+          aw[g][i] = fmaf(dy[i], xh, aw[g][i]);
+          ab[g][i] += dy[i];
+          s[2 * r] += dyw;
+          s[2 * r + 1] = fmaf(dyw, xh, s[2 * r + 1]);
         }
       }
     }
@@ -263,14 +318,22 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
         for (int g = 0; g < G; ++g) {
           const int at = (l + g * p.tpr) * VEC;
           if (at < p.D) {
+            float x[VEC], dy[VEC], wr[VEC];
+            cur.x[r][g].get(x);
+            cur.dy[r][g].get(dy);
+            if constexpr (!KEEP) norm_weight<VEC>(p.w, at, 1.0f, wr);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-              x[r][g][i] = rstd[r] * (dy[r][g][i] - mg - x[r][g][i] * mgx);
-            norm_store<VEC>(dx + at, x[r][g]);
+            for (int i = 0; i < VEC; ++i) {
+              const float xh = (x[i] - cur.mean[r]) * cur.rstd[r];
+              const float dyw = dy[i] * (KEEP ? w[KEEP ? g : 0][i] : wr[i]);
+              x[i] = cur.rstd[r] * (dyw - mg - xh * mgx);
+            }
+            norm_store<VEC>(dx + at, x);
           }
         }
       }
     }
+    if (AHEAD) cur = nxt;
   }
 
   // one partial sum per column and CTA
