@@ -41,15 +41,12 @@ LaIn la_in(const void* p, const int64_t* s, int H, int Hx) {
   return LaIn{p, s[0], s[1], s[2], H / Hx};
 }
 
-pararnn_status_t la_launch_recurrent(const LaParams& lp, bool bf16, cudaStream_t st) {
+pararnn_status_t la_launch_recurrent(const LaParams& lp, cudaStream_t st) {
   int dv = 0;
   for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
   const dim3 grid((unsigned)((long long)lp.B * lp.H), (unsigned)((dv + 31) / 32),
                   (unsigned)lp.npass);
-  if (bf16)
-    pararnn_linattn_recurrent_kernel<__nv_bfloat16><<<grid, kLaRecThreads, 0, st>>>(lp);
-  else
-    pararnn_linattn_recurrent_kernel<float><<<grid, kLaRecThreads, 0, st>>>(lp);
+  pararnn_linattn_recurrent_kernel<<<grid, kLaRecThreads, 0, st>>>(lp);
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }
 
@@ -168,7 +165,7 @@ pararnn_status_t la_launch(LaParams& lp, const LaPlan& pl, float* span_ws,
                            const pararnn_options_t* opts, int32_t* status_dev, cudaStream_t st) {
   lp.nspan = pl.nspan;
   lp.span = pl.span;
-  if (pl.recurrent) return la_launch_recurrent(lp, true, st);
+  if (pl.recurrent) return la_launch_recurrent(lp, st);
   if (pl.nspan > 1)
     for (int i = 0; i < lp.npass; ++i) {
       lp.pass[i].s_span = span_ws;
@@ -420,5 +417,12 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   a.o_f32 = dtype == PARARNN_F32;
   a.c_out = d->scale;
   a.c_kv = 1.0f;
-  return la_launch_recurrent(lp, dtype == PARARNN_BF16, static_cast<cudaStream_t>(stream));
+  const long long grid = d->B * d->H * ((d->Dv + 31) / 32);
+  if (grid >= (1LL << 31)) return PARARNN_ERR_INVALID_ARGUMENT;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == PARARNN_BF16)
+    pararnn_linattn_step_kernel<__nv_bfloat16><<<(unsigned)grid, kLaStepThreads, 0, st>>>(lp);
+  else
+    pararnn_linattn_step_kernel<float><<<(unsigned)grid, kLaStepThreads, 0, st>>>(lp);
+  return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }

@@ -59,7 +59,7 @@ NormShape norm_shape(bool vec, int64_t D, int warp_groups, int cta_groups, int m
   }
   s.cta = true;
   s.groups = cta_groups;
-  if (n > 512LL * cta_groups) s.groups = most_groups;
+  while (s.groups < most_groups && 512LL * s.groups < n) s.groups *= 2;
   s.tpr = 64;
   while (s.tpr < 512 && (int64_t)s.tpr * s.groups < n) s.tpr *= 2;
   s.fits = (int64_t)s.tpr * s.groups >= n;
@@ -115,13 +115,13 @@ void norm_bwd_go(NormParams& np, const NormShape& sh, cudaStream_t st) {
 
 template <typename TX, typename TY>
 void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
-  const NormShape sh = vec ? norm_shape(true, np.D, 2, 2, 4) : norm_shape(false, np.D, 16, 16, 16);
+  const NormShape sh = vec ? norm_shape(true, np.D, 1, 1, 4) : norm_shape(false, np.D, 16, 16, 16);
   if (!sh.fits) {
     np.nparts = (int)(np.M < kNormSms ? np.M : kNormSms);
     pararnn_norm_long_dx_kernel<TX, TY><<<(unsigned)np.M, 1024, 0, st>>>(np);
     pararnn_norm_long_dw_kernel<TX, TY>
         <<<dim3((unsigned)((np.D + 127) / 128), (unsigned)np.nparts), 128, 0, st>>>(np);
-    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 256, 0, st>>>(np);
+    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 32 * kNormSlices, 0, st>>>(np);
     return;
   }
   if (vec) {
@@ -135,7 +135,7 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
     norm_bwd_go<TX, TY, 1, 16, 1>(np, sh, st);
   }
   if (np.nparts > 1)
-    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 256, 0, st>>>(np);
+    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 32 * kNormSlices, 0, st>>>(np);
 }
 
 }  // namespace

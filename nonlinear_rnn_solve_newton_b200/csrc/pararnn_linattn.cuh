@@ -94,8 +94,7 @@ __device__ __forceinline__ double la_pow(float log_decay, int i) { return la_pow
 // walk the tokens, kLaRecT at a time: the tokens' q, k and v are staged in shared
 // memory as fp32, every thread updates its rows and adds up its part of q S, and
 // the row groups' parts are joined once per batch of tokens.  All arithmetic is
-// fp32.  One token (the decode step) is the case L = 1: it reads and writes the
-// state once and is bound by that traffic.
+// fp32.
 // ---------------------------------------------------------------------------
 constexpr int kLaRecT = 8;
 constexpr int kLaRecCols = 32;
@@ -109,7 +108,7 @@ template <int COLS> struct LaWalkSmem {
 
 // Tokens [tb, tb + n) of (b, h), columns c0 .. c0 + COLS - 1, state at element
 // (r, c) of s_in + r sr + c sc (NULL = 0); the state behind them to s_out (dense).
-template <typename T, int COLS, int THREADS>
+template <int COLS, int THREADS>
 __device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, int h, int c0,
                                      long long tb, long long n, const float* s_in, long long sr,
                                      long long sc, float* s_out, LaWalkSmem<COLS>& sm) {
@@ -147,9 +146,9 @@ __device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, 
     }
   }
 
-  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
-  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
-  const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
   const long long obase = b * a.ob + h * a.oh;
   const long long first = a.rev ? tb + n - 1 : tb;
   const int dir = a.rev ? -1 : 1;
@@ -223,7 +222,6 @@ __device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, 
   }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kLaRecThreads)
     pararnn_linattn_recurrent_kernel(const __grid_constant__ LaParams p) {
   __shared__ LaWalkSmem<kLaRecCols> sm;
@@ -233,7 +231,7 @@ __global__ void __launch_bounds__(kLaRecThreads)
   const int b = (int)(blockIdx.x / p.H), h = (int)(blockIdx.x % p.H);
   const long long n = la_length(p, b);
   const long long sb = ((long long)b * p.H + h) * a.dk * a.dv;
-  la_walk<T, kLaRecCols, kLaRecThreads>(p, a, b, h, c0, 0, n, a.s_in ? a.s_in + sb : nullptr, a.s_r,
+  la_walk<kLaRecCols, kLaRecThreads>(p, a, b, h, c0, 0, n, a.s_in ? a.s_in + sb : nullptr, a.s_r,
                                         a.s_c, a.s_out ? a.s_out + sb : nullptr, sm);
   if (p.zero_tail) {
     const int warp = threadIdx.x >> 5, d = c0 + (threadIdx.x & 31);
@@ -245,6 +243,80 @@ __global__ void __launch_bounds__(kLaRecThreads)
         else
           static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(0.0f);
       }
+  }
+}
+
+// One token (the decode step): s_next = gamma s + k^T v, o = c_out q s_next.  Bound by
+// the state's traffic, 8 dk dv bytes per (b, h).  A CTA has a 32-column tile of the
+// states of one (b, h): 8 lanes x float4 across, 32 rows down, at most 4 rows a
+// thread, all of whose loads are issued before anything is waited for; the small
+// vectors come straight from global memory.  In place is fine: each element is read
+// and written by the same thread.
+constexpr int kLaStepThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kLaStepThreads)
+    pararnn_linattn_step_kernel(const __grid_constant__ LaParams p) {
+  __shared__ float4 s_part[kLaStepThreads / 32][8];
+  const LaPass& a = p.pass[0];
+  const int tiles = (a.dv + 31) / 32;
+  const int bh = (int)(blockIdx.x / tiles), c0 = (int)(blockIdx.x % tiles) * 32;
+  const int b = bh / p.H, h = bh % p.H;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cg = lane & 7, rg = warp * 4 + (lane >> 3), col = c0 + cg * 4;
+  const bool cok = col < a.dv;
+  const long long sb = (long long)bh * a.dk * a.dv;
+  float4 s[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = r * 32 + rg;
+    s[r] = a.s_in && cok && row < a.dk
+               ? __ldcs(reinterpret_cast<const float4*>(a.s_in + sb + row * a.dv + col))
+               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
+  const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
+  const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (cok) x = make_float4(la_load(v + col), la_load(v + col + 1), la_load(v + col + 2), la_load(v + col + 3));
+  float kk[4], qq[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = r * 32 + rg;
+    kk[r] = row < a.dk ? la_load(k + row) : 0.0f;
+    qq[r] = row < a.dk ? la_load(q + row) : 0.0f;
+  }
+  const float gamma = expf(p.log_decay[h]);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = r * 32 + rg;
+    const float4 w = make_float4(fmaf(kk[r], x.x, gamma * s[r].x), fmaf(kk[r], x.y, gamma * s[r].y),
+                                 fmaf(kk[r], x.z, gamma * s[r].z), fmaf(kk[r], x.w, gamma * s[r].w));
+    o = make_float4(fmaf(qq[r], w.x, o.x), fmaf(qq[r], w.y, o.y), fmaf(qq[r], w.z, o.z),
+                    fmaf(qq[r], w.w, o.w));
+    if (cok && row < a.dk) *reinterpret_cast<float4*>(a.s_out + sb + row * a.dv + col) = w;
+  }
+#pragma unroll
+  for (int m = 8; m < 32; m <<= 1) {
+    o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
+    o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
+    o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
+    o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
+  }
+  if (lane < 8) s_part[warp][lane] = o;
+  __syncthreads();
+  if (threadIdx.x < 32 && c0 + threadIdx.x < a.dv) {
+    float y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLaStepThreads / 32; ++w)
+      y += reinterpret_cast<const float*>(s_part[w])[threadIdx.x];
+    y *= a.c_out;
+    const long long at = b * a.ob + h * a.oh + c0 + threadIdx.x;
+    if (a.o_f32)
+      static_cast<float*>(a.o)[at] = y;
+    else
+      static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(y);
   }
 }
 

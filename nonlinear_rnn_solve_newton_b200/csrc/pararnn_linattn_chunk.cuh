@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (s_fail) return;
   if (FULL && s_bad) {
     if (threadIdx.x < kLaAgainThreads)
-      la_walk<__nv_bfloat16, kLaN, kLaAgainThreads>(
+      la_walk<kLaN, kLaAgainThreads>(
           p, a, b, h, col0, tb, len, s_in ? s_in + sb : nullptr, sr, sc,
           s_out ? s_out + sb : nullptr, *reinterpret_cast<LaWalkSmem<kLaN>*>(dsmem));
   } else if (warp >= 10 && s_out && row < a.dk) {

@@ -227,7 +227,10 @@ template <typename T> struct NormRaw<T, 1> {
 // R rows at a time, and the next R on their way while these are worked on: what is in
 // flight covers the latency of HBM.  The rows stay as they lie in memory and are
 // unpacked twice (for the sums, and for dx), which costs fewer registers than keeping
-// them as fp32.
+// them as fp32.  Measured on B200 (both kernels, us, floor in brackets): 262144 x 128
+// bf16 48 (31), 32768 x 1024 fp32 x 67 (51), 16384 x 4096 fp32 x, bf16 dy 129 (103).
+// One group of 8 a thread: two groups 49 / 78 / 144 us; R = 1 49 / 76 / 141; R = 4
+// spills, 218 at D = 4096; two sets of rows in turn instead of the copy 49 / 74 / 168.
 template <typename TX, typename TY, int VEC, int G, int R, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
     pararnn_norm_bwd_kernel(const __grid_constant__ NormParams p) {
@@ -275,15 +278,9 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
       }
     }
   };
-  int turn = 0;
   const long long lead = blockIdx.x * (long long)rpc + (CTA ? 0 : warp * rpw);  // uniform in a warp
   const long long own = CTA ? 0 : lane / p.tpr;
-  constexpr bool AHEAD = G * VEC <= 16;  // (four groups a thread leave no room for a second set)
-  Rows cur, nxt;
-  if (AHEAD) fetch(cur, lead + own);
-  for (long long r0 = lead; r0 < p.M; r0 += R * stride) {
-    const long long row0 = r0 + own;
-    fetch(AHEAD ? nxt : cur, AHEAD ? row0 + R * stride : row0);
+  const auto work = [&](const Rows& cur, long long row0, int turn) {
     float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -307,7 +304,6 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
       }
     }
     norm_sum<2 * R, CTA>(s, p.tpr, sm, turn);
-    turn ^= 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r * stride;
@@ -333,7 +329,24 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
         }
       }
     }
-    if (AHEAD) cur = nxt;
+  };
+  const long long step = R * stride;
+  if constexpr (G * VEC <= 16) {
+    Rows one, two;
+    int turn = 0;
+    fetch(one, lead + own);
+    for (long long r0 = lead; r0 < p.M; r0 += step, turn ^= 1) {
+      fetch(two, r0 + own + step);
+      work(one, r0 + own, turn);
+      one = two;
+    }
+  } else {  // four groups a thread leave no room for a second set
+    Rows one;
+    int turn = 0;
+    for (long long r0 = lead; r0 < p.M; r0 += step, turn ^= 1) {
+      fetch(one, r0 + own);
+      work(one, r0 + own, turn);
+    }
   }
 
   // one partial sum per column and CTA
@@ -384,16 +397,29 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
   }
 }
 
-// The CTAs' sums, joined in a fixed order: 32 columns x 8 slices of the parts.
-__global__ void __launch_bounds__(256) pararnn_norm_join_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float sm[8][2][32];
+// The CTAs' sums, joined in a fixed order: 32 columns x 32 slices of the parts, a
+// slice's loads all in flight (with 8 slices in turn this took 31 us at D = 128,
+// as long as the pass itself).
+constexpr int kNormSlices = 32;
+__global__ void __launch_bounds__(32 * kNormSlices)
+    pararnn_norm_join_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[kNormSlices][2][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
   float sw = 0.0f, sb = 0.0f;
   if (d < p.D) {
-#pragma unroll 4
-    for (int i = slice; i < p.nparts; i += 8) {
-      sw += p.part[(long long)i * p.D + d];
-      sb += p.part[(long long)(p.nparts + i) * p.D + d];
+    for (int i0 = slice; i0 < p.nparts; i0 += 8 * kNormSlices) {
+      float w[8], b[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = i0 + k * kNormSlices;
+        w[k] = i < p.nparts ? __ldcg(p.part + (long long)i * p.D + d) : 0.0f;
+        b[k] = i < p.nparts ? __ldcg(p.part + (long long)(p.nparts + i) * p.D + d) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sw += w[k];
+        sb += b[k];
+      }
     }
   }
   sm[slice][0][lane] = sw;
@@ -402,7 +428,7 @@ __global__ void __launch_bounds__(256) pararnn_norm_join_kernel(const __grid_con
   if (slice < 2 && d < p.D) {
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += sm[i][slice][lane];
+    for (int i = 0; i < kNormSlices; ++i) s += sm[i][slice][lane];
     (slice ? p.db : p.dw)[d] = s;
   }
 }
