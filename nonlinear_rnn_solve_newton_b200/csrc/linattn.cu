@@ -417,12 +417,21 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   a.o_f32 = dtype == PARARNN_F32;
   a.c_out = d->scale;
   a.c_kv = 1.0f;
-  const long long grid = d->B * d->H * ((d->Dv + 31) / 32);
-  if (grid >= (1LL << 31)) return PARARNN_ERR_INVALID_ARGUMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == PARARNN_BF16)
-    pararnn_linattn_step_kernel<__nv_bfloat16><<<(unsigned)grid, kLaStepThreads, 0, st>>>(lp);
+  // tiles of 4096 elements, 4 rows a thread: 128 rows x 32 columns, or 64 x 64 (with 32
+  // columns half of the threads would have no rows: 256 x 32 states of 64 x 64 76 us)
+  const bool low = d->Dk <= 64;
+  const long long cols = low ? 64 : 32, grid = d->B * d->H * ((d->Dv + cols - 1) / cols);
+  if (grid >= (1LL << 31)) return PARARNN_ERR_INVALID_ARGUMENT;
+  const bool bf16 = dtype == PARARNN_BF16;
+  const dim3 g((unsigned)grid);
+  if (bf16 && low)
+    pararnn_linattn_step_kernel<__nv_bfloat16, 64, 64><<<g, kLaStepThreads, 0, st>>>(lp);
+  else if (bf16)
+    pararnn_linattn_step_kernel<__nv_bfloat16, 32, 128><<<g, kLaStepThreads, 0, st>>>(lp);
+  else if (low)
+    pararnn_linattn_step_kernel<float, 64, 64><<<g, kLaStepThreads, 0, st>>>(lp);
   else
-    pararnn_linattn_step_kernel<float><<<(unsigned)grid, kLaStepThreads, 0, st>>>(lp);
+    pararnn_linattn_step_kernel<float, 32, 128><<<g, kLaStepThreads, 0, st>>>(lp);
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }

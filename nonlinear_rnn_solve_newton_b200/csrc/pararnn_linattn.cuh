@@ -247,29 +247,31 @@ __global__ void __launch_bounds__(kLaRecThreads)
 }
 
 // One token (the decode step): s_next = gamma s + k^T v, o = c_out q s_next.  Bound by
-// the state's traffic, 8 dk dv bytes per (b, h).  A CTA has a 32-column tile of the
-// states of one (b, h): 8 lanes x float4 across, 32 rows down, at most 4 rows a
+// the state's traffic, 8 dk dv bytes per (b, h).  A CTA has a tile of COLS columns of
+// the state of one (b, h): COLS / 4 lanes x float4 across, the rest down, R rows a
 // thread, all of whose loads are issued before anything is waited for; the small
 // vectors come straight from global memory.  In place is fine: each element is read
-// and written by the same thread.
+// and written by the same thread.  Measured on B200 at 192 x 32 states of 128 x 128 (the
+// floor is 123 us): tiles of 32 columns 143 us, whole rows of 128 (16 rows a thread) 158.
 constexpr int kLaStepThreads = 256;
 
-template <typename T>
+template <typename T, int COLS, int ROWS>
 __global__ void __launch_bounds__(kLaStepThreads)
     pararnn_linattn_step_kernel(const __grid_constant__ LaParams p) {
-  __shared__ float4 s_part[kLaStepThreads / 32][8];
+  constexpr int CG = COLS / 4, RG = kLaStepThreads / CG, R = ROWS / RG;
+  __shared__ float4 s_part[kLaStepThreads / 32][CG];
   const LaPass& a = p.pass[0];
-  const int tiles = (a.dv + 31) / 32;
-  const int bh = (int)(blockIdx.x / tiles), c0 = (int)(blockIdx.x % tiles) * 32;
+  const int tiles = (a.dv + COLS - 1) / COLS;
+  const int bh = (int)(blockIdx.x / tiles), c0 = (int)(blockIdx.x % tiles) * COLS;
   const int b = bh / p.H, h = bh % p.H;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cg = lane & 7, rg = warp * 4 + (lane >> 3), col = c0 + cg * 4;
+  const int cg = lane % CG, rg = (int)threadIdx.x / CG, col = c0 + cg * 4;
   const bool cok = col < a.dv;
   const long long sb = (long long)bh * a.dk * a.dv;
-  float4 s[4];
+  float4 s[R];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = r * 32 + rg;
+  for (int r = 0; r < R; ++r) {
+    const int row = r * RG + rg;
     s[r] = a.s_in && cok && row < a.dk
                ? __ldcs(reinterpret_cast<const float4*>(a.s_in + sb + row * a.dv + col))
                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -279,18 +281,18 @@ __global__ void __launch_bounds__(kLaStepThreads)
   const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (cok) x = make_float4(la_load(v + col), la_load(v + col + 1), la_load(v + col + 2), la_load(v + col + 3));
-  float kk[4], qq[4];
+  float kk[R], qq[R];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = r * 32 + rg;
+  for (int r = 0; r < R; ++r) {
+    const int row = r * RG + rg;
     kk[r] = row < a.dk ? la_load(k + row) : 0.0f;
     qq[r] = row < a.dk ? la_load(q + row) : 0.0f;
   }
   const float gamma = expf(p.log_decay[h]);
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = r * 32 + rg;
+  for (int r = 0; r < R; ++r) {
+    const int row = r * RG + rg;
     const float4 w = make_float4(fmaf(kk[r], x.x, gamma * s[r].x), fmaf(kk[r], x.y, gamma * s[r].y),
                                  fmaf(kk[r], x.z, gamma * s[r].z), fmaf(kk[r], x.w, gamma * s[r].w));
     o = make_float4(fmaf(qq[r], w.x, o.x), fmaf(qq[r], w.y, o.y), fmaf(qq[r], w.z, o.z),
@@ -298,15 +300,15 @@ __global__ void __launch_bounds__(kLaStepThreads)
     if (cok && row < a.dk) *reinterpret_cast<float4*>(a.s_out + sb + row * a.dv + col) = w;
   }
 #pragma unroll
-  for (int m = 8; m < 32; m <<= 1) {
+  for (int m = CG; m < 32; m <<= 1) {
     o.x += __shfl_xor_sync(0xffffffffu, o.x, m);
     o.y += __shfl_xor_sync(0xffffffffu, o.y, m);
     o.z += __shfl_xor_sync(0xffffffffu, o.z, m);
     o.w += __shfl_xor_sync(0xffffffffu, o.w, m);
   }
-  if (lane < 8) s_part[warp][lane] = o;
+  if (lane < CG) s_part[warp][lane] = o;
   __syncthreads();
-  if (threadIdx.x < 32 && c0 + threadIdx.x < a.dv) {
+  if (threadIdx.x < COLS && c0 + threadIdx.x < a.dv) {
     float y = 0.0f;
 #pragma unroll
     for (int w = 0; w < kLaStepThreads / 32; ++w)
