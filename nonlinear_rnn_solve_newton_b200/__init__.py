@@ -865,13 +865,11 @@ def rollout_lstm(P, a, c0=None, h0=None, out=None, stream=None):
     return c, h
 
 
-def _stream_tensor(name, t, dtype, shape, unit):
+def _stream_strides(name, t, dtype, shape, unit):
     """Checks one stream of a linear-attention call and returns its element
     strides.  The last axis is contiguous; with ``unit`` > 1 every stride is a
-    positive multiple of it and the first element is aligned to it (what the
-    tensor copies need).  An axis of size 1 takes the stride of a dense layout."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    positive multiple of it (what the tensor copies need).  An axis of size 1
+    takes the stride of a dense layout."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     sizes, strides = t.shape, list(t.stride())
@@ -889,35 +887,73 @@ def _stream_tensor(name, t, dtype, shape, unit):
                              f"got {tuple(t.stride())}")
         else:
             dense *= n
-    if unit > 1 and t.data_ptr() % (unit * t.element_size()):
-        raise ValueError(f"{name} must start on a {unit * t.element_size()}-byte boundary")
-    return strides[:-1]
+    strides = strides[:-1]
+    if len(strides) == 2:  # one token: its stride is not used
+        strides.insert(1, 0)
+    return _Stride3(*strides)
 
 
-def _linattn_shapes(q, k, v, log_decay, scale, dtype, unit, tokens):
+_linattn_descs = {}
+
+
+def _linattn_desc(q, k, v, log_decay, scale, dtype, do=None):
     """The call's descriptor from its tensors ([B, L, heads, size], or [B, heads,
-    size] for one token)."""
-    nd = 4 if tokens else 3
-    if q.dim() != nd or k.dim() != nd or v.dim() != nd or log_decay.dim() != 1:
-        raise ValueError("q, k, v must be [B, L, heads, size] and log_decay [H]" if tokens else
-                         "q, k, v must be [B, heads, size] and log_decay [H]")
-    lead = tuple(q.shape[:-2])
-    Hq, Dk = q.shape[-2:]
-    Hk, (Hv, Dv), H = k.shape[-2], v.shape[-2:], log_decay.shape[0]
-    if H == 0 or min(Hq, Hk, Hv) == 0 or H % Hq or H % Hk or H % Hv:
-        raise ValueError(f"the heads of q, k and v ({Hq}, {Hk}, {Hv}) must divide the {H} heads "
-                         "of log_decay")
-    if Dk % 8 or Dv % 8 or not 8 <= Dk <= 128 or not 8 <= Dv <= 128:
-        raise ValueError(f"head sizes must be multiples of 8 from 8 to 128, got {Dk} and {Dv}")
-    qs = _stream_tensor("q", q, dtype, lead + (Hq, Dk), unit)
-    ks = _stream_tensor("k", k, dtype, lead + (Hk, Dk), unit)
-    vs = _stream_tensor("v", v, dtype, lead + (Hv, Dv), unit)
-    if not tokens:  # the token's stride is not used
-        for st in (qs, ks, vs):
-            st.insert(1, 0)
-    _check_dev("log_decay", log_decay, torch.float32, (H,))
-    return _LinAttn(lead[0], lead[1] if tokens else 1, H, Hq, Hk, Hv, Dk, Dv, scale, 0,
-                    _Stride3(*qs), _Stride3(*ks), _Stride3(*vs))
+    size] for one token), remembered per shapes, strides and types.  Scans need
+    strides and first elements on 16-byte units."""
+    tokens = q.dim() == 4
+    key = (q.shape, k.shape, v.shape, log_decay.shape, q.stride(), k.stride(), v.stride(),
+           log_decay.stride(), q.dtype, k.dtype, v.dtype, log_decay.dtype, dtype, scale,
+           None if do is None else (do.shape, do.stride(), do.dtype))
+    d = _linattn_descs.get(key)
+    if d is None:
+        if q.dim() not in (3, 4) or k.dim() != q.dim() or v.dim() != q.dim() \
+                or log_decay.dim() != 1:
+            raise ValueError("q, k, v must be [B, L, heads, size] ([B, heads, size] for one "
+                             "token) and log_decay [H]")
+        lead, unit = tuple(q.shape[:-2]), 8 if tokens else 1
+        Hq, Dk = q.shape[-2:]
+        Hk, (Hv, Dv), H = k.shape[-2], v.shape[-2:], log_decay.shape[0]
+        if H == 0 or min(Hq, Hk, Hv) == 0 or H % Hq or H % Hk or H % Hv:
+            raise ValueError(f"the heads of q, k and v ({Hq}, {Hk}, {Hv}) must divide the {H} "
+                             "heads of log_decay")
+        if Dk % 8 or Dv % 8 or not 8 <= Dk <= 128 or not 8 <= Dv <= 128:
+            raise ValueError(f"head sizes must be multiples of 8 from 8 to 128, got {Dk} and {Dv}")
+        if log_decay.dtype != torch.float32:
+            raise TypeError(f"log_decay: expected {torch.float32}, got {log_decay.dtype}")
+        if not log_decay.is_contiguous():
+            raise ValueError("log_decay must be contiguous")
+        d = _LinAttn(lead[0], lead[1] if tokens else 1, H, Hq, Hk, Hv, Dk, Dv, scale, 0,
+                     _stream_strides("q", q, dtype, lead + (Hq, Dk), unit),
+                     _stream_strides("k", k, dtype, lead + (Hk, Dk), unit),
+                     _stream_strides("v", v, dtype, lead + (Hv, Dv), unit))
+        if do is not None:
+            d.do_stride = _stream_strides("do", do, dtype, lead + (H, Dv), unit)
+        if len(_linattn_descs) > 1024:
+            _linattn_descs.clear()
+        _linattn_descs[key] = d
+    if tokens:
+        for name, t in (("q", q), ("k", k), ("v", v), ("do", do)):
+            if t is not None and t.data_ptr() % 16:
+                raise ValueError(f"{name} must start on a 16-byte boundary")
+    return d
+
+
+def _linattn_ws(lib, d, backward):
+    """Workspace bytes of a scan with this descriptor: the library's answer, remembered
+    like those of the solves."""
+    key = ("linattn", d.B, d.L, d.H, d.Hq, d.Hk, d.Hv, d.Dk, d.Dv, backward)
+    n = _ws_sizes.get(key)
+    if n is None:
+        n = int(lib.pararnn_linattn_workspace_size(ctypes.byref(d), backward))
+        if len(_ws_sizes) > 4096:
+            _ws_sizes.clear()
+        _ws_sizes[key] = n
+    return n
+
+
+def _making_on(stream):
+    """Where a call's own outputs are made: on the stream that it runs on."""
+    return _same_device if stream is None else torch.cuda.stream(stream)
 
 
 def _call_buffer(nbytes, device, stream):
@@ -926,9 +962,7 @@ def _call_buffer(nbytes, device, stream):
     so that captured graphs keep workspaces of their own."""
     if nbytes <= 256:
         return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
+    with _making_on(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
@@ -949,23 +983,27 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     at and after a row's length are not used; their rows of o are left as they were
     in ``out`` and are zero in a tensor this call makes.  ``state_out`` may be s0."""
     lib = load()
-    d = _linattn_shapes(q, k, v, log_decay, scale, torch.bfloat16, 8, True)
+    if q.dim() != 4:
+        raise ValueError("q, k, v must be [B, L, heads, size]")
+    d = _linattn_desc(q, k, v, log_decay, float(scale), torch.bfloat16)
     B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
     _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
     _check_dev("lengths", lengths, torch.int32, (B,))
-    if out is None:
-        make = torch.empty if lengths is None else torch.zeros
-        out = make((B, L, H, Dv), dtype=torch.bfloat16, device=q.device)
-    if state_out is None:
-        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
-    elif s0 is not None and state_out.data_ptr() != s0.data_ptr() and _overlap(state_out, s0):
+    given = state_out is not None
+    with _making_on(stream):
+        if out is None:
+            make = torch.empty if lengths is None else torch.zeros
+            out = make((B, L, H, Dv), dtype=torch.bfloat16, device=q.device)
+        if state_out is None:
+            state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    if given and s0 is not None and state_out.data_ptr() != s0.data_ptr() and _overlap(state_out, s0):
         raise ValueError("state_out must be s0 itself or not overlap it")
     _check_dev("out", out, torch.bfloat16, (B, L, H, Dv))
     _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
     _check_dev("status", status, torch.int32, (1,))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s0=s0, lengths=lengths, out=out,
                       state_out=state_out, status=status)
-    nws = lib.pararnn_linattn_workspace_size(ctypes.byref(d), 0)
+    nws = _linattn_ws(lib, d, 0)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
         st = lib.pararnn_scan_linattn(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
@@ -984,16 +1022,18 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     and v, summed over the heads that share one; ds0 [B, H, Dk, Dv] fp32).  Rows at and
     after a batch row's length get zeros.  The decay is a constant of the layer."""
     lib = load()
-    d = _linattn_shapes(q, k, v, log_decay, scale, torch.bfloat16, 8, True)
+    if q.dim() != 4 or do.dim() != 4:
+        raise ValueError("q, k, v and do must be [B, L, heads, size]")
+    d = _linattn_desc(q, k, v, log_decay, float(scale), torch.bfloat16, do)
     B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
-    d.do_stride[:] = _stream_tensor("do", do, torch.bfloat16, (B, L, H, Dv), 8)
     _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
     _check_dev("ds", ds, torch.float32, (B, H, Dk, Dv))
     _check_dev("lengths", lengths, torch.int32, (B,))
     if out is None:
-        dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
-                      for t in (q, k, v))
-        ds0 = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+        with _making_on(stream):
+            dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
+                          for t in (q, k, v))
+            ds0 = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
     else:
         dq, dk, dv, ds0 = out
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
@@ -1004,7 +1044,7 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     _check_dev("status", status, torch.int32, (1,))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
                       dq=dq, dk=dk, dv=dv, ds0=ds0, status=status)
-    nws = lib.pararnn_linattn_workspace_size(ctypes.byref(d), 1)
+    nws = _linattn_ws(lib, d, 1)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
         st = lib.pararnn_scan_linattn_backward(
@@ -1026,14 +1066,18 @@ def step_linattn(q, k, v, log_decay, s_prev=None, scale=1.0, out=None, state_out
     dt = F32 if q.dtype == torch.float32 else BF16
     if q.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"q must be float32 or bfloat16, got {q.dtype}")
-    d = _linattn_shapes(q, k, v, log_decay, scale, q.dtype, 1, False)
+    if q.dim() != 3:
+        raise ValueError("q, k, v must be [B, heads, size]")
+    d = _linattn_desc(q, k, v, log_decay, float(scale), q.dtype)
     B, H, Dk, Dv = d.B, d.H, d.Dk, d.Dv
     _check_dev("s_prev", s_prev, torch.float32, (B, H, Dk, Dv))
-    if out is None:
-        out = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
-    if state_out is None:
-        state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
-    elif s_prev is not None and state_out.data_ptr() != s_prev.data_ptr() \
+    given = state_out is not None
+    with _making_on(stream):
+        if out is None:
+            out = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
+        if state_out is None:
+            state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+    if given and s_prev is not None and state_out.data_ptr() != s_prev.data_ptr() \
             and _overlap(state_out, s_prev):
         raise ValueError("state_out must be s_prev itself or not overlap it")
     _check_dev("out", out, q.dtype, (B, H, Dv))
@@ -1095,10 +1139,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, st
         out_dtype = x.dtype if out is None else out.dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out_dtype must be float32 or bfloat16")
-    y = torch.empty(x.shape, dtype=out_dtype, device=x.device) if out is None else out
+    with _making_on(stream):
+        y = torch.empty(x.shape, dtype=out_dtype, device=x.device) if out is None else out
+        mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2)) \
+            if stats is None else stats
     _check_dev("out", y, out_dtype, x.shape)
-    mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2)) \
-        if stats is None else stats
     _check_dev("mean", mean, torch.float32, lead)
     _check_dev("rstd", rstd, torch.float32, lead)
     dev = _one_device(x=x, weight=weight, bias=bias, out=y, mean=mean, rstd=rstd)
@@ -1125,8 +1170,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     _check_dev("mean", mean, torch.float32, lead)
     _check_dev("rstd", rstd, torch.float32, lead)
     if out is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw, db = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
+        with _making_on(stream):
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dw, db = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
     else:
         dx, dw, db = out
     _check_dev("dx", dx, x.dtype, x.shape)

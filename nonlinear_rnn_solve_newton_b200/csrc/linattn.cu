@@ -2,6 +2,7 @@
 // include/pararnn.h): argument validation, workspace layout and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -87,26 +88,38 @@ bool la_map(CUtensorMap* m, const LaIn& in, int D, const LaParams& lp) {
   return la_map(m, in.p, in.st, in.sh, in.sb, D, lp.H / in.rep, lp);
 }
 
-template <int KD, bool FULL, bool F32>
+template <int KD, bool FULL, bool BWD>
 pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStream_t st) {
-  const void* fn = (const void*)pararnn_linattn_chunk_kernel<KD, FULL, F32>;
+  // the kernel's shared memory has been raised on these devices (by index)
+  static std::atomic<unsigned long long> raised{0};
+  const void* fn = (const void*)pararnn_linattn_chunk_kernel<KD, FULL, BWD>;
   const size_t smem = LaSmem<KD>::kBytes;
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess) {
-    cudaGetLastError();
-    return PARARNN_ERR_UNSUPPORTED;
-  }
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return PARARNN_ERR_CUDA;
-  }
   int dv = 0;
   for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
   const dim3 grid((unsigned)((long long)lp.B * lp.H * lp.nspan),
                   (unsigned)((dv + kLaN - 1) / kLaN), (unsigned)lp.npass);
-  pararnn_linattn_chunk_kernel<KD, FULL, F32><<<grid, kLaThreads, smem, st>>>(lp, tm);
-  return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PARARNN_ERR_CUDA;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  // a second try where the first launch is refused: a device that was reset since has
+  // forgotten the setting
+  for (bool known = (raised.load(std::memory_order_relaxed) & bit) != 0;; known = false) {
+    if (!known) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction
+                   ? PARARNN_ERR_UNSUPPORTED
+                   : PARARNN_ERR_CUDA;
+      }
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+    pararnn_linattn_chunk_kernel<KD, FULL, BWD><<<grid, kLaThreads, smem, st>>>(lp, tm);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return PARARNN_OK;
+    if (!known) return PARARNN_ERR_CUDA;
+  }
 }
 
 // The launches of one call.
@@ -119,10 +132,8 @@ pararnn_status_t la_walks(const LaParams& lp, const LaMaps& tm, cudaStream_t st)
                                   256, 0, st>>>(lp);
     if (cudaGetLastError() != cudaSuccess) return PARARNN_ERR_CUDA;
   }
-  bool f32 = false;
-  for (int i = 0; i < lp.npass; ++i) f32 = f32 || lp.pass[i].o_f32;
-  return f32 ? la_launch_chunk<KD, true, true>(lp, tm, st)
-             : la_launch_chunk<KD, true, false>(lp, tm, st);
+  return lp.npass > 1 ? la_launch_chunk<KD, true, true>(lp, tm, st)
+                      : la_launch_chunk<KD, true, false>(lp, tm, st);
 }
 
 // The form of a call and, for the chunked form, the spans that time is cut into.
@@ -148,7 +159,7 @@ LaPlan la_plan(const pararnn_linattn_t* d, bool backward, const pararnn_options_
   // in units of one chunk's walk: a CTA costs about two to start; with more than one
   // span the states are walked first (two thirds of the work) and two more kernels start
   double best = 0.0;
-  for (long long want = 1; want <= chunks && want <= kLaSms; ++want) {
+  for (long long want = 1; want <= chunks && (want - 1) * items <= 2 * kLaSms; ++want) {
     const long long len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
     const long long waves = (items * n + kLaSms - 1) / kLaSms;
     const double cost = n > 1 ? waves * (1.67 * len + 4.0) + 6.0 : waves * (len + 2.0);

@@ -17,18 +17,19 @@
 //   local   O_a  = P V             128 x 64 x 128    P from TMEM
 // V1 + V2 + V3 are three bf16 pieces of the weighted v (24 bits, so the state
 // is as exact as fp32 sums make it); they lie side by side, so that one N = 192
-// product reads K^T once for all three.  P (the weighted scores) and the copy of
+// product reads K^T once for all three.  A pass whose state nobody gets (dq and dk)
+// takes two pieces: the 2^-17 that they leave is far below the bf16 of its output.
+// P (the weighted scores) and the copy of
 // S that Q multiplies are rounded to bf16: two independent roundings of terms of
 // an output that is itself rounded to bf16.
 //
 // Roles: warp 0 tensor copies (q, k, v of a chunk, two stages each; the output
-// tile, staged where the chunk's v was), warp 1 issues the products, warps 2-9 weight the scores and write the outputs, warps 10-17
-// carry the state, weight v and write the state's bf16 copy.  Two warps share a
-// TMEM lane quarter and split its columns: with four warps a role, each
-// instruction was fetched for a single warp of an SM quarter and a third of the
-// issue slots waited for instructions.  The scores of the next chunk are made
-// before the local output of this one, so that weighting them (the longest step
-// outside the tensor cores) is off the path.  Every wait is bounded.
+// tile, staged where the chunk's v was), warp 1 issues the products, warps 2-9
+// weight the scores and write the outputs, warps 10-17 carry the state, weight v
+// and write the state's bf16 copy.  Two warps share a TMEM lane quarter and split
+// its columns: with four warps a role, each instruction was fetched for a single
+// warp of an SM quarter and a third of the issue slots waited for instructions.
+// Every wait is bounded.
 //
 // TMEM (512 columns): two buffers of 128 for the scores -- the weighted scores
 // replace the lower half of a buffer, the local output then takes the upper --
@@ -245,7 +246,8 @@ __device__ __forceinline__ void sts128(unsigned a, unsigned x, unsigned y, unsig
                : "memory");
 }
 
-template <int KD, bool FULL, bool F32>
+// BWD: a pass of the backward call, whose output may be fp32 and whose state unwanted.
+template <int KD, bool FULL, bool BWD>
 __global__ void __launch_bounds__(kLaThreads, 1)
     pararnn_linattn_chunk_kernel(const __grid_constant__ LaParams p,
                                  const __grid_constant__ LaMaps tm) {
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int tb = (int)(span * p.span), len = (int)la_span_tokens(p, b, span);  // L < 2^31
   const int nc = (len + kLaT - 1) / kLaT;
   const float ld = p.log_decay[h];
-  const bool rev = a.rev != 0;
+  const bool rev = a.rev != 0, three = !BWD || a.s_out != nullptr;  // pieces of v
   // the state before this span and behind it: element (r, c) at r s_r + c s_c
   const long long sb = (p.nspan > 1 ? (long long)blockIdx.x : bh) * a.dk * a.dv;
   const float* s_in = !FULL ? nullptr : p.nspan > 1 ? a.s_span : a.s_in;
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
   // whether a chunk's output goes out as one tensor store: bf16, and no row of the
   // tile that must stay as it is (the store clips at L itself)
-  const bool tail_staged = n_tail == kLaT || tb + len == p.L, bf16_out = !(F32 && a.o_f32);
+  const bool tail_staged = n_tail == kLaT || tb + len == p.L, bf16_out = !(BWD && a.o_f32);
   const auto staged = [&](int c) { return bf16_out && (c != c_tail || tail_staged); };
 
   // the state, and its bf16 copy's halves, belong to warps 10-17
@@ -438,8 +440,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         if (la_elect()) {
 #pragma unroll
           for (int i = 0; i < kLaT / 16; ++i)
-            umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u, la_idesc(192, true, true),
-                        i != 0);
+            umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u,
+                        three ? la_idesc(192, true, true) : la_idesc(128, true, true), i != 0);
           umma_commit(&s_kv[st]);
         }
         __syncwarp();
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int i = row;
     const long long obase = (long long)b * a.ob + (long long)h * a.oh + col0;
     const int nd = a.dv - col0 < kLaN ? a.dv - col0 : kLaN;
-    const bool f32 = F32 && a.o_f32;
+    const bool f32 = BWD && a.o_f32;
     // this row's factor of the carried output, in a full chunk and in the last one
     const float e_full = a.c_out * (float)la_pow(ld, rev ? kLaT - 1 - i : i + 1);
     const float e_tail =
@@ -663,13 +665,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           unsigned u1[16], u2[16], u3[16];
           tmem_ld16_async(t_kv + lane_off + 32 * hf + 16 * part, u1);
           tmem_ld16_async(t_kv + lane_off + 32 * hf + 64 + 16 * part, u2);
-          tmem_ld16_async(t_kv + lane_off + 32 * hf + 128 + 16 * part, u3);
+          if (three) tmem_ld16_async(t_kv + lane_off + 32 * hf + 128 + 16 * part, u3);
           tmem_wait_ld();
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
             const f32x2 old = s[8 * part + d];
-            const f32x2 low = fma2(
-                hh2, old, add2(pair2u(u3[2 * d], u3[2 * d + 1]), pair2u(u2[2 * d], u2[2 * d + 1])));
+            f32x2 low = pair2u(u2[2 * d], u2[2 * d + 1]);
+            if (three) low = add2(low, pair2u(u3[2 * d], u3[2 * d + 1]));
+            low = fma2(hh2, old, low);
             s[8 * part + d] = fma2(hh1, old, add2(pair2u(u1[2 * d], u1[2 * d + 1]), low));
           }
         }
@@ -713,12 +716,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           const f32x2 z = fma2(pair2(bf16_lo(w1[g]), bf16_hi(w1[g])), minus, y);
           unpair2(z, z0, z1);
           w2[g] = pack_bf16(z0, z1);
-          unpair2(fma2(pair2(bf16_lo(w2[g]), bf16_hi(w2[g])), minus, z), z0, z1);
-          w3[g] = pack_bf16(z0, z1);
+          if (three) {
+            unpair2(fma2(pair2(bf16_lo(w2[g]), bf16_hi(w2[g])), minus, z), z0, z1);
+            w3[g] = pack_bf16(z0, z1);
+          }
         }
         sts128(unit[j] + Sm::kVw, w1[0], w1[1], w1[2], w1[3]);
         sts128(unit[j] + Sm::kVw + kLaBlk, w2[0], w2[1], w2[2], w2[3]);
-        sts128(unit[j] + Sm::kVw + 2 * kLaBlk, w3[0], w3[1], w3[2], w3[3]);
+        if (three) sts128(unit[j] + Sm::kVw + 2 * kLaBlk, w3[0], w3[1], w3[2], w3[3]);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
