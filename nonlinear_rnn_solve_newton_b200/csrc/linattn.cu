@@ -137,9 +137,11 @@ pararnn_status_t la_walks(const LaParams& lp, const LaMaps& tm, cudaStream_t st)
 }
 
 // The form of a call and, for the chunked form, the spans that time is cut into.
-// The recurrent form takes about a microsecond per 8 tokens whatever the batch, the
-// chunked one a few microseconds per 128.
-constexpr long long kLaRecurrentMax = 16;
+// The recurrent form's time grows with every token, the chunked one's with every 128.
+// Scan, one launch in a graph, recurrent / chunked: one sequence of 8 heads of 128 at 8
+// tokens 8.8 / 9.9 us, at 16 14.2 / 9.9; 8 x 16 heads of 128 at 8 tokens 14.1 / 19.1, at
+// 16 23.6 / 18.9; 32 x 16 heads of 64 at 8 tokens 16.9 / 30.9, at 16 27.3 / 30.8.
+constexpr long long kLaRecurrentMax = 8;
 constexpr long long kLaSms = 148;  // one CTA of the chunked form each
 
 struct LaPlan {
