@@ -93,7 +93,7 @@ pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStrea
   // the kernel's shared memory has been raised on these devices (by index)
   static std::atomic<unsigned long long> raised{0};
   const void* fn = (const void*)pararnn_linattn_chunk_kernel<KD, FULL, BWD>;
-  const size_t smem = LaSmem<KD>::kBytes;
+  const size_t smem = LaSmem<KD>::bytes(FULL);
   int dv = 0;
   for (int i = 0; i < lp.npass; ++i) dv = lp.pass[i].dv > dv ? lp.pass[i].dv : dv;
   const dim3 grid((unsigned)((long long)lp.B * lp.H * lp.nspan),
@@ -115,7 +115,11 @@ pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStrea
       }
       raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    pararnn_linattn_chunk_kernel<KD, FULL, BWD><<<grid, kLaThreads, smem, st>>>(lp, tm);
+    if (FULL && lp.nspan > 1)  // behind the join
+      launch_behind(pararnn_linattn_chunk_kernel<KD, FULL, BWD>, grid, dim3(kLaThreads), smem, st,
+                    lp, tm);
+    else
+      pararnn_linattn_chunk_kernel<KD, FULL, BWD><<<grid, kLaThreads, smem, st>>>(lp, tm);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) return PARARNN_OK;
     if (!known) return PARARNN_ERR_CUDA;
@@ -126,11 +130,18 @@ pararnn_status_t la_launch_chunk(const LaParams& lp, const LaMaps& tm, cudaStrea
 template <int KD>
 pararnn_status_t la_walks(const LaParams& lp, const LaMaps& tm, cudaStream_t st) {
   if (lp.nspan > 1) {
-    const pararnn_status_t rc = la_launch_chunk<KD, false, false>(lp, tm, st);
+    const pararnn_status_t rc = lp.npass > 1 ? la_launch_chunk<KD, false, true>(lp, tm, st)
+                                             : la_launch_chunk<KD, false, false>(lp, tm, st);
     if (rc != PARARNN_OK) return rc;
-    pararnn_linattn_join_kernel<<<dim3((unsigned)((long long)lp.B * lp.H), 8, (unsigned)lp.npass),
-                                  256, 0, st>>>(lp);
-    if (cudaGetLastError() != cudaSuccess) return PARARNN_ERR_CUDA;
+    int n = 0;
+    for (int i = 0; i < lp.npass; ++i) n = lp.pass[i].dk * lp.pass[i].dv;  // the same in all
+    const dim3 grid((unsigned)((long long)lp.B * lp.H),
+                    (unsigned)((n + kLaJoinThreads - 1) / kLaJoinThreads), (unsigned)lp.npass);
+    if (launch_behind(pararnn_linattn_join_kernel, grid, dim3(kLaJoinThreads), 0, st, lp) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return PARARNN_ERR_CUDA;
+    }
   }
   return lp.npass > 1 ? la_launch_chunk<KD, true, true>(lp, tm, st)
                       : la_launch_chunk<KD, true, false>(lp, tm, st);

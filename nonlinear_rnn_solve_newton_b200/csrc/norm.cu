@@ -69,8 +69,9 @@ NormShape norm_shape(bool vec, int64_t D, int warp_groups, int cta_groups, int m
 template <typename TX, typename TY, int VEC, int G>
 void norm_fwd_go(NormParams& np, const NormShape& sh, cudaStream_t st) {
   np.tpr = sh.tpr;
-  if (sh.cta) {
-    pararnn_norm_kernel<TX, TY, VEC, G, true><<<(unsigned)np.M, sh.tpr, 0, st>>>(np);
+  if (sh.cta) {  // always with the most groups
+    if constexpr (VEC == 1 || G == 4)
+      pararnn_norm_kernel<TX, TY, VEC, G, true><<<(unsigned)np.M, sh.tpr, 0, st>>>(np);
   } else {
     const long long rows = (long long)(kNormThreads / 32) * (32 / sh.tpr);
     pararnn_norm_kernel<TX, TY, VEC, G, false>
@@ -106,11 +107,17 @@ void norm_bwd_go(NormParams& np, const NormShape& sh, cudaStream_t st) {
   if (most > norm_max_parts(np.D)) most = norm_max_parts(np.D);
   const long long want = (np.M + rows - 1) / rows;
   np.nparts = (int)(want < most ? want : most);
+  // vectors are held by whole warps one group a lane
   if (sh.cta)
     pararnn_norm_bwd_kernel<TX, TY, VEC, G, R, true><<<np.nparts, sh.tpr, 0, st>>>(np);
-  else
+  else if constexpr (VEC == 1 || G == 1)
     pararnn_norm_bwd_kernel<TX, TY, VEC, G, R, false>
         <<<np.nparts, kNormThreads, 8 * (size_t)np.D, st>>>(np);
+}
+
+void norm_join(const NormParams& np, cudaStream_t st) {
+  launch_behind(pararnn_norm_join_kernel, dim3((unsigned)((np.D + 31) / 32)),
+                dim3(32 * kNormSlices), 0, st, np);
 }
 
 template <typename TX, typename TY>
@@ -121,7 +128,7 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
     pararnn_norm_long_dx_kernel<TX, TY><<<(unsigned)np.M, 1024, 0, st>>>(np);
     pararnn_norm_long_dw_kernel<TX, TY>
         <<<dim3((unsigned)((np.D + 127) / 128), (unsigned)np.nparts), 128, 0, st>>>(np);
-    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 32 * kNormSlices, 0, st>>>(np);
+    norm_join(np, st);
     return;
   }
   if (vec) {
@@ -135,7 +142,7 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
     norm_bwd_go<TX, TY, 1, 16, 1>(np, sh, st);
   }
   if (np.nparts > 1)
-    pararnn_norm_join_kernel<<<(unsigned)((np.D + 31) / 32), 32 * kNormSlices, 0, st>>>(np);
+    norm_join(np, st);
 }
 
 }  // namespace

@@ -43,11 +43,14 @@
 // Spans: where (batch row, head, tile) give fewer CTAs than SMs, time is cut into
 // spans.  A first launch (FULL = false) computes the state that each span's own
 // tokens leave, pararnn_linattn_join_kernel carries them over the spans, and the
-// walk starts each span from the state before it.
+// walk starts each span from the state before it.  In the first launch warps 2-9 weight
+// v, into two places in turn, and the update has two buffers, so that weights, product
+// and state work on three chunks at a time.
 #pragma once
 
 #include "pararnn_linattn.cuh"
 #include "pararnn_proj.cuh"
+#include "pararnn_sm100.cuh"
 
 namespace pararnn {
 
@@ -68,7 +71,11 @@ template <int KD> struct LaSmem {
   static constexpr unsigned kVw = kV + 2 * kLaBlk;                    // 3 blocks
   static constexpr unsigned kS = kVw + 3 * kLaBlk;                    // KD rows x 128 B
   static constexpr unsigned kEnd = kS + KD * 128;
-  static constexpr size_t kBytes = kEnd + 1024;  // + alignment slack
+  // a second place for weighted v where no q and no outputs are made (FULL = false)
+  static constexpr unsigned kVw2 = KD == 128 ? kQ : kEnd;
+  static constexpr size_t bytes(bool full) {  // with alignment slack
+    return kEnd + 1024 + (full || KD == 128 ? 0 : 3 * kLaBlk);
+  }
 };
 
 struct LaMaps {
@@ -198,31 +205,6 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, unsigned sr
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// Two fp32 operations in one instruction, on a pair of neighbouring registers.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair2(float x, float y) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-  return d;
-}
-__device__ __forceinline__ void unpair2(f32x2 d, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ f32x2 pair2u(unsigned x, unsigned y) {
   return pair2(__uint_as_float(x), __uint_as_float(y));
 }
@@ -254,7 +236,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   using Sm = LaSmem<KD>;
   extern __shared__ __align__(1024) unsigned char dsmem[];
   __shared__ unsigned long long s_full[2], s_vfull[2], s_pv[2], s_put[2], s_sc[2],
-      s_rd[4], s_p, s_kv[2], s_qs[2], s_b, s_go, s_pad, s_drain;
+      s_rd[4], s_p, s_kv[2], s_qs[2], s_b, s_go[2], s_pad, s_drain;
   // c_out c_kv gamma^d by distance d, in the order in which a row's columns need it:
   // forwards d = 127 - x, backwards d = x - 32; 0 for the 32 distances below 0.  A second
   // copy, one place on and 16 banks off, is for rows whose first place is odd: every
@@ -291,13 +273,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       mbar_init(&s_pv[s], 1);
       mbar_init(&s_put[s], 256);
       mbar_init(&s_sc[s], 1);
+      mbar_init(&s_go[s], 256);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&s_rd[s], 32);
     mbar_init(&s_drain, 1);
     mbar_init(&s_p, 256);
     mbar_init(&s_b, 512);
     mbar_init(&s_pad, 256);
-    mbar_init(&s_go, 256);
     s_fail = 0;
     s_bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -323,6 +305,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  wait_for_launch_before();
   const unsigned tmem = s_tmem;
   const unsigned t_sc = tmem, t_kv = tmem + 256, t_oi = tmem + 448;
   // token of row 0 of the c-th chunk walked, and its number of tokens
@@ -345,6 +328,65 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
   for (int j = 0; j < 4; ++j) unit[j] = sbase + la_unit(0u, row, 4 * hf + j);
 
+  // the update of chunk c: two buffers where no scores are made
+  const auto t_up = [&](int c) { return FULL ? t_kv : tmem + 256u * (unsigned)(c & 1); };
+  // Weighted v of chunk c, in three (two) pieces: thread = token, half of the columns;
+  // vfull, vtail: the token's weight in a full chunk and in the last one.  False where a
+  // wait ran out.
+  const auto weight = [&](int n) {
+    return row < n ? a.c_kv * (float)la_pow(ld, rev ? row + 1 : n - 1 - row) : 0.0f;
+  };
+  const auto weigh = [&](int c, float vfull, float vtail) {
+    const int st = c & 1, n = rows(c);
+    bool ok = la_wait(&s_vfull[st], (unsigned)(c >> 1) & 1u, limit);
+    if (ok && n < kLaT) ok = la_wait(&s_full[st], (unsigned)(c >> 1) & 1u, limit);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const unsigned vw = FULL || !st ? Sm::kVw : Sm::kVw2;
+    const unsigned vb = Sm::kV + st * kLaBlk;
+    float f = vfull;
+    if (n < kLaT) {
+      f = vtail;
+      if (row >= n) {  // padding of v and k: whatever it holds becomes zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sts128(unit[j] + vb, 0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int m = 0; m < KD / 64; ++m)
+            sts128(unit[j] + Sm::kK + (st * (KD / 64) + m) * kLaBlk, 0u, 0u, 0u, 0u);
+        }
+      }
+    }
+    const f32x2 ff = pair2(f, f), minus = pair2(-1.0f, -1.0f);
+    uint4 in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) in[j] = lds128(unit[j] + vb);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned v4[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
+      unsigned w1[4], w2[4], w3[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x2 y = mul2(pair2(bf16_lo(v4[g]), bf16_hi(v4[g])), ff);
+        float y0, y1, z0, z1;
+        unpair2(y, y0, y1);
+        w1[g] = pack_bf16(y0, y1);
+        const f32x2 z = fma2(pair2(bf16_lo(w1[g]), bf16_hi(w1[g])), minus, y);
+        unpair2(z, z0, z1);
+        w2[g] = pack_bf16(z0, z1);
+        if (three) {
+          unpair2(fma2(pair2(bf16_lo(w2[g]), bf16_hi(w2[g])), minus, z), z0, z1);
+          w3[g] = pack_bf16(z0, z1);
+        }
+      }
+      sts128(unit[j] + vw, w1[0], w1[1], w1[2], w1[3]);
+      sts128(unit[j] + vw + kLaBlk, w2[0], w2[1], w2[2], w2[3]);
+      if (three) sts128(unit[j] + vw + 2 * kLaBlk, w3[0], w3[1], w3[2], w3[3]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    return true;
+  };
+
   if (warp == 0) {
     if (lane == 0) {
       // ---- tensor copies ----------------------------------------------------------
@@ -360,6 +402,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         bool ok = true;
         // each buffer as soon as chunk c - 2 has no more use for it: k, q, then v, where
         // that chunk's output is staged
+        if (!FULL && c < nc) {  // v is of no use once it has been weighted
+          if (c >= 2) ok = la_wait(&s_go[st], before, limit);
+          if (!ok) break;
+          mbar_expect_tx(&s_vfull[st], kLaBlk);
+          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+        }
         if (c < nc) {
           if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
           if (!ok) break;
@@ -385,8 +433,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           }
         }
         if (c < nc) {
-          mbar_expect_tx(&s_vfull[st], kLaBlk);
-          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          if (FULL) {
+            mbar_expect_tx(&s_vfull[st], kLaBlk);
+            tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          }
           done = c + 1;
         }
         if (c + kLaAhead < nc) {
@@ -417,7 +467,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                              dkt0 = umma_desc_mn_sw128(sbase + Sm::kK),
                              dv0 = umma_desc_mn_sw128(sbase + Sm::kV),
                              dw = umma_desc_mn_sw128(sbase + Sm::kVw),
-                             ds = umma_desc_mn_sw128(sbase + Sm::kS);
+                             ds = umma_desc_mn_sw128(sbase + Sm::kS),
+                             dw2 = umma_desc_mn_sw128(sbase + Sm::kVw2) - dw;
     // the whole warp waits; true in every lane or in none
     const auto wait = [&](unsigned long long* bar, unsigned parity) {
       const bool ok = la_wait(bar, parity, limit);
@@ -432,15 +483,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const unsigned stq = st * (KD / 64) * (kLaBlk >> 4);
       if (c >= 0) {
-        // weighted v is there, the last update has been read
-        ok = wait(&s_go, par);
-        if (ok && !FULL) ok = wait(&s_full[st], par2);
+        // weighted v is there, the last update from the same columns has been read
+        if (!FULL) ok = wait(&s_full[st], par2) && (c < 2 || wait(&s_put[st], par2 ^ 1u));
+        ok = ok && wait(&s_go[st], par2);
         if (!ok) break;
         tc_fence_after();
         if (la_elect()) {
 #pragma unroll
           for (int i = 0; i < kLaT / 16; ++i)
-            umma_f16_ss(t_kv, dkt0 + stq + i * 128u, dw + i * 128u,
+            umma_f16_ss(t_up(c), dkt0 + stq + i * 128u, dw + (FULL || !st ? 0u : dw2) + i * 128u,
                         three ? la_idesc(192, true, true) : la_idesc(128, true, true), i != 0);
           umma_commit(&s_kv[st]);
         }
@@ -494,6 +545,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     __syncwarp();
     const long long last = limit < 2000000000LL ? 2000000000LL : limit;
     la_wait(&s_drain, 0u, last);
+  } else if (!FULL && warp < 10) {
+    // ---- weighted v, one chunk ahead of its product -----------------------------------
+    const float vfull = weight(kLaT), vtail = weight(n_tail);
+    for (int c = 0; c < nc; ++c) {
+      // the place has been read
+      bool ok = c < 2 || la_wait(&s_kv[c & 1], (unsigned)((c >> 1) - 1) & 1u, limit);
+      ok = __all_sync(0xffffffffu, ok) && weigh(c, vfull, vtail);
+      if (!ok) {
+        s_fail = 1;
+        break;
+      }
+      mbar_arrive(&s_go[c & 1]);
+    }
   } else if (warp < 10) {
     // ---- weighted scores and outputs: thread = token, half of the columns -----------
     const int i = row;
@@ -506,8 +570,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         i < n_tail ? a.c_out * (float)la_pow(ld, rev ? n_tail - 1 - i : i + 1) : 0.0f;
     const int x0 = rev ? 32 - i : 127 - i;
     const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
-    if (FULL && nc > 0) mbar_arrive(&s_b);  // chunk 0 has no outputs before it
-    for (int c = 0; FULL && c < nc; ++c) {
+    if (nc > 0) mbar_arrive(&s_b);  // chunk 0 has no outputs before it
+    for (int c = 0; c < nc; ++c) {
       const int st = c & 1;
       const unsigned par = (unsigned)c & 1u, par2 = (unsigned)(c >> 1) & 1u;
       const int n = rows(c);
@@ -612,7 +676,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       mbar_arrive(&s_put[st]);
     }
-    if (FULL && p.zero_tail && !*(volatile int*)&s_fail) {
+    if (p.zero_tail && !*(volatile int*)&s_fail) {
       const long long end = span == p.nspan - 1 ? p.L : tb + p.span;
       for (long long t = (long long)tb + len + i; t < end; t += kLaT)
         for (int d = 8 * hf; d < nd; d += 16) {
@@ -641,10 +705,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     }
     float ghi, glo;  // gamma^128
     la_two(la_pow(ld, kLaT), ghi, glo);
-    // this row's weight of v, in a full chunk and in the last one
-    const float vfull = a.c_kv * (float)la_pow(ld, rev ? r + 1 : kLaT - 1 - r);
-    const float vtail =
-        r < n_tail ? a.c_kv * (float)la_pow(ld, rev ? r + 1 : n_tail - 1 - r) : 0.0f;
+    const float vfull = FULL ? weight(kLaT) : 0.0f, vtail = FULL ? weight(n_tail) : 0.0f;
     bool ok = true;
     for (int c = 0; c <= nc; ++c) {
       const int st = c & 1;
@@ -663,9 +724,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           unsigned u1[16], u2[16], u3[16];
-          tmem_ld16_async(t_kv + lane_off + 32 * hf + 16 * part, u1);
-          tmem_ld16_async(t_kv + lane_off + 32 * hf + 64 + 16 * part, u2);
-          if (three) tmem_ld16_async(t_kv + lane_off + 32 * hf + 128 + 16 * part, u3);
+          const unsigned t_u = t_up(c - 1) + lane_off + 32 * hf + 16 * part;
+          tmem_ld16_async(t_u, u1);
+          tmem_ld16_async(t_u + 64, u2);
+          if (three) tmem_ld16_async(t_u + 128, u3);
           tmem_wait_ld();
 #pragma unroll
           for (int d = 0; d < 8; ++d) {
@@ -677,59 +739,18 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           }
         }
       }
+      if (!FULL && c > 0) {
+        tc_fence_before();
+        mbar_arrive(&s_put[st ^ 1]);
+      }
       if (c == nc) break;
-      const int n = rows(c);
-      ok = la_wait(&s_vfull[st], (unsigned)(c >> 1) & 1u, limit);
-      if (ok && n < kLaT) ok = la_wait(&s_full[st], (unsigned)(c >> 1) & 1u, limit);
-      if (!__all_sync(0xffffffffu, ok)) {
+      if (!FULL) continue;
+      if (!weigh(c, vfull, vtail)) {
         ok = false;
         break;
       }
-      const unsigned vb = Sm::kV + st * kLaBlk;
-      float f = vfull;
-      if (n < kLaT) {
-        f = vtail;
-        if (r >= n) {  // padding of v and k: whatever it holds becomes zero
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sts128(unit[j] + vb, 0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int m = 0; m < KD / 64; ++m)
-              sts128(unit[j] + Sm::kK + (st * (KD / 64) + m) * kLaBlk, 0u, 0u, 0u, 0u);
-          }
-        }
-      }
-      const f32x2 ff = pair2(f, f), minus = pair2(-1.0f, -1.0f);
-      uint4 in[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) in[j] = lds128(unit[j] + vb);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned v4[4] = {in[j].x, in[j].y, in[j].z, in[j].w};
-        unsigned w1[4], w2[4], w3[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x2 y = mul2(pair2(bf16_lo(v4[g]), bf16_hi(v4[g])), ff);
-          float y0, y1, z0, z1;
-          unpair2(y, y0, y1);
-          w1[g] = pack_bf16(y0, y1);
-          const f32x2 z = fma2(pair2(bf16_lo(w1[g]), bf16_hi(w1[g])), minus, y);
-          unpair2(z, z0, z1);
-          w2[g] = pack_bf16(z0, z1);
-          if (three) {
-            unpair2(fma2(pair2(bf16_lo(w2[g]), bf16_hi(w2[g])), minus, z), z0, z1);
-            w3[g] = pack_bf16(z0, z1);
-          }
-        }
-        sts128(unit[j] + Sm::kVw, w1[0], w1[1], w1[2], w1[3]);
-        sts128(unit[j] + Sm::kVw + kLaBlk, w2[0], w2[1], w2[2], w2[3]);
-        if (three) sts128(unit[j] + Sm::kVw + 2 * kLaBlk, w3[0], w3[1], w3[2], w3[3]);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc_fence_before();
-      mbar_arrive(&s_go);
-      if (FULL && n < kLaT) mbar_arrive(&s_pad);
-      if (!FULL) continue;
+      mbar_arrive(&s_go[st]);
+      if (rows(c) < kLaT) mbar_arrive(&s_pad);
       if (c > 0) {  // the last copy of the state has been read
         ok = la_wait(&s_qs[st ^ 1], (unsigned)((c - 1) >> 1) & 1u, limit);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -796,28 +817,40 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
 // The states that the spans' own tokens leave (s_span, [B, H, spans, dk, dv]) become the
 // states before the spans; the state behind the last one goes to s_out.
-__global__ void pararnn_linattn_join_kernel(const __grid_constant__ LaParams p) {
+constexpr int kLaJoinThreads = 256;
+constexpr int kLaJoinAhead = 8;  // spans whose states are on their way at a time
+
+__global__ void __launch_bounds__(kLaJoinThreads)
+    pararnn_linattn_join_kernel(const __grid_constant__ LaParams p) {
   const LaPass& a = p.pass[blockIdx.z];
   const int bh = blockIdx.x, b = bh / p.H;
   const float ld = p.log_decay[bh % p.H];
-  const int n = a.dk * a.dv;
+  const int n = a.dk * a.dv, e = (int)(threadIdx.x + blockIdx.y * kLaJoinThreads);
   float ghi, glo;  // of a whole span
   la_two(la_powl(ld, p.span), ghi, glo);
-  for (int e = threadIdx.x + blockIdx.y * blockDim.x; e < n; e += blockDim.x * gridDim.y) {
-    const int r = e / a.dv, c = e % a.dv;
-    float x = a.s_in ? a.s_in[(long long)bh * n + r * a.s_r + c * a.s_c] : 0.0f;
-    float* sp = a.s_span + (long long)bh * p.nspan * n + e;
-    for (int k = 0; k < p.nspan; ++k) {
-      const int g = a.rev ? p.nspan - 1 - k : k;
+  wait_for_launch_before();
+  if (e >= n) return;
+  const int r = e / a.dv, c = e % a.dv;
+  float x = a.s_in ? a.s_in[(long long)bh * n + r * a.s_r + c * a.s_c] : 0.0f;
+  float* sp = a.s_span + (long long)bh * p.nspan * n + e;
+  for (int k0 = 0; k0 < p.nspan; k0 += kLaJoinAhead) {
+    float own[kLaJoinAhead];
+#pragma unroll
+    for (int i = 0; i < kLaJoinAhead; ++i)
+      if (k0 + i < p.nspan)
+        own[i] = sp[(long long)(a.rev ? p.nspan - 1 - k0 - i : k0 + i) * n];
+#pragma unroll
+    for (int i = 0; i < kLaJoinAhead; ++i) {
+      if (k0 + i >= p.nspan) break;
+      const int g = a.rev ? p.nspan - 1 - k0 - i : k0 + i;
       const long long m = la_span_tokens(p, b, g);
       float h1 = ghi, h2 = glo;
       if (m != p.span) la_two(la_powl(ld, m), h1, h2);
-      const float own = sp[(long long)g * n];
       sp[(long long)g * n] = x;
-      x = m == 0 ? x : fmaf(h1, x, fmaf(h2, x, own));
+      x = m == 0 ? x : fmaf(h1, x, fmaf(h2, x, own[i]));
     }
-    if (a.s_out) a.s_out[(long long)bh * n + e] = x;
   }
+  if (a.s_out) a.s_out[(long long)bh * n + e] = x;
 }
 
 }  // namespace pararnn

@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pararnn_sm100.cuh"
+
 namespace pararnn {
 
 struct NormParams {
@@ -188,6 +190,41 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads)
   }
 }
 
+// A group's elements as the arithmetic takes them: four pairs, or one number.
+template <int VEC> struct NormVal;
+template <> struct NormVal<8> {
+  using T = f32x2;
+  static constexpr int N = 4;
+};
+template <> struct NormVal<1> {
+  using T = float;
+  static constexpr int N = 1;
+};
+__device__ __forceinline__ float nadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float nmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float nfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f32x2 nadd(f32x2 a, f32x2 b) { return add2(a, b); }
+__device__ __forceinline__ f32x2 nmul(f32x2 a, f32x2 b) { return mul2(a, b); }
+__device__ __forceinline__ f32x2 nfma(f32x2 a, f32x2 b, f32x2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ void nset(float& d, float v) { d = v; }
+__device__ __forceinline__ void nset(f32x2& d, float v) { d = pair2(v, v); }
+__device__ __forceinline__ float nsum(float v) { return v; }
+__device__ __forceinline__ float nsum(f32x2 v) {
+  float x, y;
+  unpair2(v, x, y);
+  return x + y;
+}
+__device__ __forceinline__ void nget(const float* v, float* out) { out[0] = v[0]; }
+__device__ __forceinline__ void nget(const f32x2* v, float* out) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair2(v[i], out[2 * i], out[2 * i + 1]);
+}
+__device__ __forceinline__ void nput(const float* in, float* v) { v[0] = in[0]; }
+__device__ __forceinline__ void nput(const float* in, f32x2* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair2(in[2 * i], in[2 * i + 1]);
+}
+
 // A group as it lies in memory.
 template <typename T, int VEC> struct NormRaw;
 template <> struct NormRaw<float, 8> {
@@ -197,9 +234,9 @@ template <> struct NormRaw<float, 8> {
     b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void get(float* v) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  __device__ __forceinline__ void get(f32x2* v) const {
+    v[0] = pair2(a.x, a.y), v[1] = pair2(a.z, a.w);
+    v[2] = pair2(b.x, b.y), v[3] = pair2(b.z, b.w);
   }
 };
 template <> struct NormRaw<__nv_bfloat16, 8> {
@@ -208,13 +245,11 @@ template <> struct NormRaw<__nv_bfloat16, 8> {
     a = __ldcs(reinterpret_cast<const uint4*>(p));
   }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float* v) const {
+  __device__ __forceinline__ void get(f32x2* v) const {
     const unsigned u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = pair2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
   }
 };
 template <typename T> struct NormRaw<T, 1> {
@@ -243,16 +278,24 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
   const long long stride = (long long)gridDim.x * rpc;   // from one row of a thread to the next
   const int ng = p.D / VEC;
   const float inv = 1.0f / (float)p.D;
+  using V = NormVal<VEC>;
+  using T = typename V::T;
+  constexpr int N = V::N;
   constexpr bool KEEP = G * VEC <= 16;  // the weights stay in registers
-  float aw[G][VEC], ab[G][VEC], w[KEEP ? G : 1][VEC];
+  T aw[G][N], ab[G][N], w[KEEP ? G : 1][N];
+  const auto weight = [&](int at, T* out) {
+    float v[VEC];
+    norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, v);
+    nput(v, out);
+  };
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    if constexpr (KEEP) {
-      const int at = l + g * p.tpr;
-      norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, w[g]);
-    }
+    if constexpr (KEEP) weight(l + g * p.tpr, w[g]);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) aw[g][i] = ab[g][i] = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      nset(aw[g][i], 0.0f);
+      nset(ab[g][i], 0.0f);
+    }
   }
   struct Rows {
     NormRaw<TX, VEC> x[R][G];
@@ -284,47 +327,58 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
     float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[2 * r] = s[2 * r + 1] = 0.0f;
+      T sg, sgx, minus, rs;
+      nset(sg, 0.0f);
+      nset(sgx, 0.0f);
+      nset(minus, -cur.mean[r]);
+      nset(rs, cur.rstd[r]);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float x[VEC], dy[VEC], wr[VEC];
+        T x[N], dy[N], wr[N];
         cur.x[r][g].get(x);
         cur.dy[r][g].get(dy);
-        const int at = l + g * p.tpr;
-        if constexpr (!KEEP) norm_weight<VEC>(at < ng ? p.w : nullptr, at * VEC, 1.0f, wr);
+        if constexpr (!KEEP) weight(l + g * p.tpr, wr);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float xh = (x[i] - cur.mean[r]) * cur.rstd[r];
-          const float dyw = dy[i] * (KEEP ? w[KEEP ? g : 0][i] : wr[i]);
-          aw[g][i] = fmaf(dy[i], xh, aw[g][i]);
-          ab[g][i] += dy[i];
-          s[2 * r] += dyw;
-          s[2 * r + 1] = fmaf(dyw, xh, s[2 * r + 1]);
+        for (int i = 0; i < N; ++i) {
+          const T xh = nmul(nadd(x[i], minus), rs);
+          const T dyw = nmul(dy[i], KEEP ? w[KEEP ? g : 0][i] : wr[i]);
+          aw[g][i] = nfma(dy[i], xh, aw[g][i]);
+          ab[g][i] = nadd(ab[g][i], dy[i]);
+          sg = nadd(sg, dyw);
+          sgx = nfma(dyw, xh, sgx);
         }
       }
+      s[2 * r] = nsum(sg);
+      s[2 * r + 1] = nsum(sgx);
     }
     norm_sum<2 * R, CTA>(s, p.tpr, sm, turn);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const long long row = row0 + r * stride;
       if (row < p.M) {
-        const float mg = s[2 * r] * inv, mgx = s[2 * r + 1] * inv;
+        T mg, mgx, minus, rs;  // the means negated
+        nset(mg, -s[2 * r] * inv);
+        nset(mgx, -s[2 * r + 1] * inv);
+        nset(minus, -cur.mean[r]);
+        nset(rs, cur.rstd[r]);
         TX* dx = static_cast<TX*>(p.y) + row * p.D;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const int at = (l + g * p.tpr) * VEC;
-          if (at < p.D) {
-            float x[VEC], dy[VEC], wr[VEC];
+          const int at = l + g * p.tpr;
+          if (at < ng) {
+            T x[N], dy[N], wr[N];
             cur.x[r][g].get(x);
             cur.dy[r][g].get(dy);
-            if constexpr (!KEEP) norm_weight<VEC>(p.w, at, 1.0f, wr);
+            if constexpr (!KEEP) weight(at, wr);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float xh = (x[i] - cur.mean[r]) * cur.rstd[r];
-              const float dyw = dy[i] * (KEEP ? w[KEEP ? g : 0][i] : wr[i]);
-              x[i] = cur.rstd[r] * (dyw - mg - xh * mgx);
+            for (int i = 0; i < N; ++i) {
+              const T xh = nmul(nadd(x[i], minus), rs);
+              const T dyw = nmul(dy[i], KEEP ? w[KEEP ? g : 0][i] : wr[i]);
+              x[i] = nmul(rs, nfma(xh, mgx, nadd(dyw, mg)));
             }
-            norm_store<VEC>(dx + at, x);
+            float out[VEC];
+            nget(x, out);
+            norm_store<VEC>(dx + at * VEC, out);
           }
         }
       }
@@ -352,14 +406,20 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
   // one partial sum per column and CTA
   float* pw = p.nparts > 1 ? p.part + (long long)blockIdx.x * p.D : p.dw;
   float* pb = p.nparts > 1 ? p.part + (long long)(p.nparts + blockIdx.x) * p.D : p.db;
+  float sw[G][VEC], sb[G][VEC];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    nget(aw[g], sw[g]);
+    nget(ab[g], sb[g]);
+  }
   if constexpr (!CTA) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         for (int t = p.tpr; t < 32; t <<= 1) {
-          aw[g][i] += __shfl_xor_sync(0xffffffffu, aw[g][i], t);
-          ab[g][i] += __shfl_xor_sync(0xffffffffu, ab[g][i], t);
+          sw[g][i] += __shfl_xor_sync(0xffffffffu, sw[g][i], t);
+          sb[g][i] += __shfl_xor_sync(0xffffffffu, sb[g][i], t);
         }
     }
     for (int w = 0; w < kNormThreads / 32; ++w) {  // the warps in turn
@@ -370,8 +430,8 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
           if (at < p.D) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-              cols[at + i] = (w ? cols[at + i] : 0.0f) + aw[g][i];
-              cols[p.D + at + i] = (w ? cols[p.D + at + i] : 0.0f) + ab[g][i];
+              cols[at + i] = (w ? cols[at + i] : 0.0f) + sw[g][i];
+              cols[p.D + at + i] = (w ? cols[p.D + at + i] : 0.0f) + sb[g][i];
             }
           }
         }
@@ -389,8 +449,8 @@ __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
       if (at < p.D) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          pw[at + i] = aw[g][i];
-          pb[at + i] = ab[g][i];
+          pw[at + i] = sw[g][i];
+          pb[at + i] = sb[g][i];
         }
       }
     }
@@ -406,6 +466,7 @@ __global__ void __launch_bounds__(32 * kNormSlices)
   __shared__ float sm[kNormSlices][2][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
   float sw = 0.0f, sb = 0.0f;
+  wait_for_launch_before();
   if (d < p.D) {
     for (int i0 = slice; i0 < p.nparts; i0 += 8 * kNormSlices) {
       float w[8], b[8];
