@@ -169,13 +169,17 @@ LaPlan la_plan(const pararnn_linattn_t* d, bool backward, const pararnn_options_
   const long long items = d->B * d->H * (backward ? 2 * tk + tv : tv);
   const long long chunks = (d->L + kLaT - 1) / kLaT;
   if (items >= 4 * kLaSms) return pl;
-  // in units of one chunk's walk: a CTA costs about two to start; with more than one
-  // span the states are walked first (two thirds of the work) and two more kernels start
+  // In units of one chunk's walk (2 us): a CTA takes about two to start and end.  With more
+  // than one span the states are walked first, 0.45 a chunk, and the join and two more
+  // launches take 4 to 7.  Measured in us, one span and the best number of them: 2048 tokens of
+  // 8 heads of 64 38.3, 20.5 (16 spans); 4096 of 16 heads of 128 67.7, 45.5 (4); 65536 of
+  // 12 heads of 64 1014, 149 (12); 4 x 4096 of 8 heads of 128 69.8, 76.7 (2: not taken).
+  const double join = d->Dk * d->Dv <= 64 * 64 ? 4.0 : 7.0;
   double best = 0.0;
   for (long long want = 1; want <= chunks && (want - 1) * items <= 2 * kLaSms; ++want) {
     const long long len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
     const long long waves = (items * n + kLaSms - 1) / kLaSms;
-    const double cost = n > 1 ? waves * (1.67 * len + 4.0) + 6.0 : waves * (len + 2.0);
+    const double cost = n > 1 ? waves * (1.45 * len + 4.0) + join : waves * (len + 2.0);
     if (want == 1 || cost < best) {
       best = cost;
       pl.nspan = (int)n;
