@@ -899,7 +899,8 @@ _linattn_descs = {}
 def _linattn_desc(q, k, v, log_decay, scale, dtype, do=None):
     """The call's descriptor from its tensors ([B, L, heads, size], or [B, heads,
     size] for one token), remembered per shapes, strides and types.  Scans need
-    strides and first elements on 16-byte units."""
+    strides and first elements on 16-byte units.  Its ``bytes`` are the extents of q, k
+    and v."""
     tokens = q.dim() == 4
     key = (q.shape, k.shape, v.shape, log_decay.shape, q.stride(), k.stride(), v.stride(),
            log_decay.stride(), q.dtype, k.dtype, v.dtype, log_decay.dtype, dtype, scale,
@@ -926,6 +927,7 @@ def _linattn_desc(q, k, v, log_decay, scale, dtype, do=None):
                      _stream_strides("q", q, dtype, lead + (Hq, Dk), unit),
                      _stream_strides("k", k, dtype, lead + (Hk, Dk), unit),
                      _stream_strides("v", v, dtype, lead + (Hv, Dv), unit))
+        d.bytes = tuple(hi - lo for lo, hi in map(_extent, (q, k, v)))
         if do is not None:
             d.do_stride = _stream_strides("do", do, dtype, lead + (H, Dv), unit)
         if len(_linattn_descs) > 1024:
@@ -966,10 +968,49 @@ def _call_buffer(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _overlap(a, b):
-    """Whether two dense tensors share any byte."""
-    x, y = a.data_ptr(), b.data_ptr()
-    return x < y + b.numel() * b.element_size() and y < x + a.numel() * a.element_size()
+def _extent(t):
+    """First byte of a tensor and the one behind its last (strides are not negative)."""
+    p = t.data_ptr()
+    if t.is_contiguous():
+        return p, p + t.nbytes
+    if t.numel() == 0:
+        return p, p
+    last = sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+    return p, p + (last + 1) * t.element_size()
+
+
+def _apart(outputs, inputs, same=()):
+    """Refuses outputs of the caller's that lie over each other or over an input, but for
+    the pairs of names in ``same``, which may be one and the same tensor."""
+    seen = [(n, *_extent(t)) for n, t in inputs if t is not None]
+    for name, t in outputs:
+        if t is None:
+            continue
+        lo, hi = _extent(t)
+        for other, lo2, hi2 in seen:
+            if lo < hi2 and lo2 < hi:
+                alias = (name, other) in same
+                if not (alias and lo == lo2):
+                    raise ValueError(f"{name} must " + (f"be {other} itself or " if alias else "")
+                                     + f"not overlap {other}")
+        seen.append((name, lo, hi))
+
+
+def _linattn_apart(d, q, k, v, log_decay, state, out, state_out, name):
+    """``_apart`` for a forward call, by numbers first: it stands before every decode step."""
+    po, ps, pi = out.data_ptr(), state_out.data_ptr(), 0 if state is None else state.data_ptr()
+    rows, item = d.B * d.H * d.Dv, out.element_size()
+    eo, es = po + rows * d.L * item, ps + rows * d.Dk * 4
+    bq, bk, bv = d.bytes
+    apart = not (po < es and ps < eo) and (pi in (0, ps) or not (ps < pi + es - ps and pi < es)) \
+        and (pi == 0 or not (po < pi + es - ps and pi < eo))
+    for u, n in ((q.data_ptr(), bq), (k.data_ptr(), bk), (v.data_ptr(), bv),
+                 (log_decay.data_ptr(), 4 * d.H)):
+        apart = apart and not (po < u + n and u < eo or ps < u + n and u < es)
+    if not apart:
+        _apart((("out", out), ("state_out", state_out)),
+               (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), (name, state)),
+               same=(("state_out", name),))
 
 
 def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None, state_out=None,
@@ -981,7 +1022,8 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     last axis contiguous), log_decay [H] fp32, s0 [B, H, Dk, Dv] fp32 or None ->
     (o [B, L, H, Dv] bf16, s [B, H, Dk, Dv] fp32).  lengths [B] int32 (device): tokens
     at and after a row's length are not used; their rows of o are left as they were
-    in ``out`` and are zero in a tensor this call makes.  ``state_out`` may be s0."""
+    in ``out`` and are zero in a tensor this call makes.  ``state_out`` may be s0; outputs
+    lie over no other argument."""
     lib = load()
     if q.dim() != 4:
         raise ValueError("q, k, v must be [B, L, heads, size]")
@@ -989,18 +1031,18 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
     _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
     _check_dev("lengths", lengths, torch.int32, (B,))
-    given = state_out is not None
+    given = out is not None or state_out is not None
     with _making_on(stream):
         if out is None:
             make = torch.empty if lengths is None else torch.zeros
             out = make((B, L, H, Dv), dtype=torch.bfloat16, device=q.device)
         if state_out is None:
             state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
-    if given and s0 is not None and state_out.data_ptr() != s0.data_ptr() and _overlap(state_out, s0):
-        raise ValueError("state_out must be s0 itself or not overlap it")
     _check_dev("out", out, torch.bfloat16, (B, L, H, Dv))
     _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
     _check_dev("status", status, torch.int32, (1,))
+    if given:
+        _linattn_apart(d, q, k, v, log_decay, s0, out, state_out, "s0")
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s0=s0, lengths=lengths, out=out,
                       state_out=state_out, status=status)
     nws = _linattn_ws(lib, d, 0)
@@ -1039,9 +1081,11 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         _check_dev(name, t, torch.bfloat16, like.shape)
     _check_dev("ds0", ds0, torch.float32, (B, H, Dk, Dv))
-    if ds is not None and _overlap(ds, ds0):
-        raise ValueError("ds0 must not overlap ds")
     _check_dev("status", status, torch.int32, (1,))
+    if out is not None:
+        _apart((("dq", dq), ("dk", dk), ("dv", dv), ("ds0", ds0)),
+               (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("do", do), ("s0", s0),
+                ("ds", ds), ("lengths", lengths)))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
                       dq=dq, dk=dk, dv=dv, ds0=ds0, status=status)
     nws = _linattn_ws(lib, d, 1)
@@ -1071,17 +1115,16 @@ def step_linattn(q, k, v, log_decay, s_prev=None, scale=1.0, out=None, state_out
     d = _linattn_desc(q, k, v, log_decay, float(scale), q.dtype)
     B, H, Dk, Dv = d.B, d.H, d.Dk, d.Dv
     _check_dev("s_prev", s_prev, torch.float32, (B, H, Dk, Dv))
-    given = state_out is not None
+    given = out is not None or state_out is not None
     with _making_on(stream):
         if out is None:
             out = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
         if state_out is None:
             state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
-    if given and s_prev is not None and state_out.data_ptr() != s_prev.data_ptr() \
-            and _overlap(state_out, s_prev):
-        raise ValueError("state_out must be s_prev itself or not overlap it")
     _check_dev("out", out, q.dtype, (B, H, Dv))
     _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
+    if given:
+        _linattn_apart(d, q, k, v, log_decay, s_prev, out, state_out, "s_prev")
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s_prev=s_prev, out=out,
                       state_out=state_out)
     with _device_guard(dev):
@@ -1107,6 +1150,8 @@ def _rows(name, t):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
     if t.dim() == 0 or t.shape[-1] == 0:
         raise ValueError(f"{name} must have a last axis of at least one element")
+    if t.is_contiguous():
+        return t.numel() // t.shape[-1], t.shape[-1]
     if t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
     rows, stride = 1, None
@@ -1132,21 +1177,29 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, st
     lib = load()
     dx = _norm_dtype("x", x)
     M, sx = _rows("x", x)
-    D, lead = x.shape[-1], tuple(x.shape[:-1])
+    D = x.shape[-1]
     _check_dev("weight", weight, torch.float32, (D,))
     _check_dev("bias", bias, torch.float32, (D,))
     if out_dtype is None:
         out_dtype = x.dtype if out is None else out.dtype
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out_dtype must be float32 or bfloat16")
+    y, (mean, rstd) = out, stats or (None, None)
     with _making_on(stream):
-        y = torch.empty(x.shape, dtype=out_dtype, device=x.device) if out is None else out
-        mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2)) \
-            if stats is None else stats
-    _check_dev("out", y, out_dtype, x.shape)
-    _check_dev("mean", mean, torch.float32, lead)
-    _check_dev("rstd", rstd, torch.float32, lead)
-    dev = _one_device(x=x, weight=weight, bias=bias, out=y, mean=mean, rstd=rstd)
+        if out is None:
+            y = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        if stats is None:
+            mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+                          for _ in range(2))
+    if out is None and stats is None:
+        dev = _one_device(x=x, weight=weight, bias=bias)
+    else:
+        _check_dev("out", y, out_dtype, x.shape)
+        _check_dev("mean", mean, torch.float32, x.shape[:-1])
+        _check_dev("rstd", rstd, torch.float32, x.shape[:-1])
+        dev = _one_device(x=x, weight=weight, bias=bias, out=y, mean=mean, rstd=rstd)
+        _apart((("out", y), ("mean", mean), ("rstd", rstd)),
+               (("x", x), ("weight", weight), ("bias", bias)))
     with _device_guard(dev):
         st = lib.pararnn_layer_norm(_ptr(x), dx, sx, _ptr(weight), _ptr(bias), _ptr(y),
                                     BF16 if out_dtype == torch.bfloat16 else F32, _ptr(mean),
@@ -1165,7 +1218,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     if tuple(dy.shape) != tuple(x.shape):
         raise ValueError(f"dy: expected shape {tuple(x.shape)}, got {tuple(dy.shape)}")
     _, sdy = _rows("dy", dy)
-    D, lead = x.shape[-1], tuple(x.shape[:-1])
+    D, lead = x.shape[-1], x.shape[:-1]
     _check_dev("weight", weight, torch.float32, (D,))
     _check_dev("mean", mean, torch.float32, lead)
     _check_dev("rstd", rstd, torch.float32, lead)
@@ -1173,13 +1226,16 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
         with _making_on(stream):
             dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
             dw, db = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
+        dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight)
     else:
         dx, dw, db = out
-    _check_dev("dx", dx, x.dtype, x.shape)
-    _check_dev("dweight", dw, torch.float32, (D,))
-    _check_dev("dbias", db, torch.float32, (D,))
-    dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dw,
-                      dbias=db)
+        _check_dev("dx", dx, x.dtype, x.shape)
+        _check_dev("dweight", dw, torch.float32, (D,))
+        _check_dev("dbias", db, torch.float32, (D,))
+        dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight, dx=dx, dweight=dw,
+                          dbias=db)
+        _apart((("dx", dx), ("dweight", dw), ("dbias", db)),
+               (("dy", dy), ("x", x), ("mean", mean), ("rstd", rstd), ("weight", weight)))
     nws = lib.pararnn_layer_norm_workspace_size(M, D)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):

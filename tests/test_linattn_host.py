@@ -261,3 +261,48 @@ def test_linattn_and_norm_refuse_cpu_tensors():
         pr.step_linattn(z(B, H, Dk), z(B, H, Dk), z(B, H, Dv), z(H, dtype=torch.float32))
     with pytest.raises(ValueError, match="CUDA"):
         pr.layer_norm(z(B, L))
+
+
+def test_outputs_over_inputs_are_refused(fake):  # noqa: F811
+    # the launches of a call read while others write: only a state may be its own output
+    f32 = torch.float32
+    q, k, v, g = qkv(k=z(B, L, H, Dk), v=z(B, L, H, Dk))
+    do = dv(z(B, L, H, Dk))
+    st, st2, m, w = (z(*s, dtype=f32) for s in ((B, H, Dk, Dk), (B, H, Dk, Dk), (6,), (8,)))
+    x, dy = dv(z(6, 8, dtype=f32)), dv(z(6, 8, dtype=f32))
+    q1, k1, v1 = (dv(z(B, H, Dk)) for _ in range(3))
+    grads = [z(B, L, H, Dk) for _ in range(3)]
+    bad = [
+        lambda: pr.scan_linattn(q, k, v, g, out=v),
+        lambda: pr.scan_linattn(q, k, v, g, out=q),
+        lambda: pr.scan_linattn(q, k, v, g, s0=st, out=k, state_out=st),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, out=(q, *grads[1:], st)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, out=(grads[0], grads[1], do, st)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, out=(grads[0], grads[1], grads[1], st)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, s0=st, out=(*grads, st)),
+        lambda: pr.step_linattn(q1, k1, v1, g, out=v1),
+        lambda: pr.step_linattn(q1, k1, v1, g, st, out=q1, state_out=st),
+        lambda: pr.layer_norm(x, w, out=x),
+        lambda: pr.layer_norm(x, w, stats=(m, m)),
+        lambda: pr.layer_norm_backward(dy, x, m, z(6, dtype=f32), out=(dy, w, z(8, dtype=f32))),
+        lambda: pr.layer_norm_backward(dy, x, m, z(6, dtype=f32), out=(x, w, z(8, dtype=f32))),
+        lambda: pr.layer_norm_backward(dy, x, m, z(6, dtype=f32), out=(z(6, 8, dtype=f32), w, w)),
+        lambda: pr.layer_norm_backward(dy, x, m, z(6, dtype=f32), w,
+                                       out=(z(6, 8, dtype=f32), w, z(8, dtype=f32))),
+    ]
+    for i, call in enumerate(bad):
+        fake.calls.clear()
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+        assert [c for c in fake.calls if "workspace_size" not in c] == [], i
+    # neighbours in one allocation, and states updated in place, are fine
+    buf = z(2 * B * L * H * Dk)
+    near = buf.view(2, B, L, H, Dk)
+    good = [
+        lambda: pr.scan_linattn(dv(near[0]), k, v, g, s0=st, out=near[1], state_out=st),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, s0=st, ds=st, out=(*grads, st2)),
+        lambda: pr.step_linattn(q1, k1, v1, g, st, state_out=st),
+        lambda: pr.layer_norm(x, w, out=z(6, 8), stats=(m, z(6, dtype=f32))),
+    ]
+    for call in good:
+        call()
