@@ -468,8 +468,12 @@ size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* desc, int32_t bac
  *  or NULL; s may be s0 itself.
  *  ws, ws_bytes: workspace of pararnn_linattn_workspace_size(desc, 0) bytes.
  *  status_dev: optional device int32 for the device-side status.
- * A non-finite v makes the whole state's column non-finite from its token on, as the
- * formula says; see the note on chunks in the source for the tokens before it.
+ *  opts->regime chooses the form: 0 automatic (recurrent up to 8 tokens), 1 recurrent
+ *  (fp32 arithmetic, a token at a time), 2 chunks of 128 tokens on the tensor cores.
+ *  Only regime and wait_timeout_ns of opts are read.
+ * Outputs must not overlap inputs or each other, but for s and s0.
+ * A token that is not finite changes nothing before it; where one occurs, or a product
+ * q.k is beyond fp32, the (batch row, head) is walked again in the recurrent form.
  * Errors: PARARNN_ERR_INVALID_ARGUMENT, _WORKSPACE, _UNSUPPORTED, _CUDA. */
 pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* desc, const void* q, const void* k,
                                       const void* v, const float* log_decay, const float* s0,
@@ -484,8 +488,9 @@ pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* desc, const void*
  * with gamma R_{n+1} read as ds.  The decay is a constant of the layer: it gets
  * no gradient.
  *  dq [B, L, Hq, Dk], dk [B, L, Hk, Dk], dv [B, L, Hv, Dv]: bf16, contiguous; rows at
- *  and after a batch row's length are set to zero.  ds0 [B, H, Dk, Dv] fp32 or NULL;
- *  it must not overlap ds.  ws: pararnn_linattn_workspace_size(desc, 1) bytes. */
+ *  and after a batch row's length are set to zero.  ds0 [B, H, Dk, Dv] fp32 or NULL.
+ *  Outputs must not overlap inputs or each other.
+ *  ws: pararnn_linattn_workspace_size(desc, 1) bytes. */
 pararnn_status_t pararnn_scan_linattn_backward(
     const pararnn_linattn_t* desc, const void* q, const void* k, const void* v,
     const float* log_decay, const float* s0, const void* dout, const float* ds,
@@ -496,7 +501,8 @@ pararnn_status_t pararnn_scan_linattn_backward(
  * o = scale q s_next.  desc->L must be 1; the strides' token entry is not used.
  *  q [B, Hq, Dk], k [B, Hk, Dk], v [B, Hv, Dv], o [B, H, Dv] (contiguous): all fp32 or
  *  all bf16 (dtype).  s_prev [B, H, Dk, Dv] fp32 or NULL (= 0); s_next the same
- *  shape and may be s_prev itself (a state cache updated in place). */
+ *  shape and may be s_prev itself (a state cache updated in place); else outputs must
+ *  not overlap inputs or each other. */
 pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* desc, const void* q, const void* k,
                                       const void* v, pararnn_dtype_t dtype,
                                       const float* log_decay, const float* s_prev, void* o,
@@ -509,6 +515,7 @@ pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* desc, const void*
  *  x [M, D] fp32 or bf16, rows x_stride elements apart (last axis contiguous);
  *  weight, bias [D] fp32 or NULL (1 and 0);  y [M, D] fp32 or bf16, contiguous;
  *  mean, rstd [M] fp32: the rows' statistics, which the backward pass reads.
+ *  Outputs (here and below) must not overlap inputs or each other.
  *  eps >= 0.  Statistics are fp32, the variance is taken about the mean.  */
 pararnn_status_t pararnn_layer_norm(const void* x, pararnn_dtype_t x_dtype, int64_t x_stride,
                                     const float* weight, const float* bias, void* y,

@@ -416,6 +416,8 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   if (dtype != PARARNN_F32 && dtype != PARARNN_BF16) return PARARNN_ERR_INVALID_ARGUMENT;
   if (d->B == 0) return PARARNN_OK;
   if (!q || !k || !v || !o || !log_decay || !s_next) return PARARNN_ERR_INVALID_ARGUMENT;
+  for (const int64_t* x : {d->q_stride, d->k_stride, d->v_stride})
+    if (x[0] < 0 || x[2] < 0) return PARARNN_ERR_INVALID_ARGUMENT;
   const size_t es = dtype == PARARNN_F32 ? 4 : 2;
   if (!la_aligned(q, es) || !la_aligned(k, es) || !la_aligned(v, es) || !la_aligned(o, es) ||
       !la_aligned(log_decay, 4) || !la_aligned(s_prev, 16) || !la_aligned(s_next, 16))

@@ -37,8 +37,10 @@
 //
 // A mask that multiplies by zero lets a non-finite k or v of a later token
 // of the chunk into an output.  Such a token also leaves the state non-finite
-// for good, so the end of the walk shows it: the CTA then walks its tokens
-// again with the recurrent form, which reads no token before its time.
+// for good, so the end of the walk shows it.  A product q.k beyond fp32 shows in the
+// weighted scores, whose largest is kept (also where v is zero or the token later,
+// so that no output should see it).  In both cases the CTA walks its tokens again with
+// the recurrent form, which reads no token before its time and makes no scores.
 //
 // Spans: where (batch row, head, tile) give fewer CTAs than SMs, time is cut into
 // spans.  A first launch (FULL = false) computes the state that each span's own
@@ -187,6 +189,12 @@ __device__ __forceinline__ void tmem_wait_st() {
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const unsigned*>(&t);
+}
+// The larger of the magnitudes, in each half; NaN where either is one.
+__device__ __forceinline__ unsigned larger_bf16x2(unsigned a, unsigned b) {
+  unsigned d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 // The box on its way into L2 (nothing waits for it).
 __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
@@ -570,6 +578,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         i < n_tail ? a.c_out * (float)la_pow(ld, rev ? n_tail - 1 - i : i + 1) : 0.0f;
     const int x0 = rev ? 32 - i : 127 - i;
     const float* wt0 = s_wt + (x0 & 1 ? kLaWt2 + x0 - 1 : x0);
+    unsigned big = 0u;  // the largest of this token's weighted scores, two columns at a time
     if (nc > 0) mbar_arrive(&s_b);  // chunk 0 has no outputs before it
     for (int c = 0; c < nc; ++c) {
       const int st = c & 1;
@@ -583,7 +592,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       tc_fence_after();
       const unsigned t_s = t_sc + lane_off + 128 * st;
       // two blocks of 32 columns; those beyond the diagonal block J = qd are zero
-      unsigned w[32];
+      unsigned w[32], most = big;
 #pragma unroll
       for (int jj = 0; jj < 2; ++jj) {
         const int J = 2 * hf + jj;
@@ -601,12 +610,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             float y0, y1;
             unpair2(mul2(pair2u(r[2 * e], r[2 * e + 1]), f[e]), y0, y1);
             w[16 * jj + e] = pack_bf16(y0, y1);
+            most = larger_bf16x2(most, w[16 * jj + e]);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[16 * jj + e] = 0u;
         }
       }
+      if (i < n) big = most;
       // the weighted scores go to columns 0-63, where the warp of the lower half reads
       tc_fence_before();
       if (hf == 0) {
@@ -676,6 +687,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       mbar_arrive(&s_put[st]);
     }
+    if ((big & 0x7F80u) == 0x7F80u || (big & 0x7F800000u) == 0x7F800000u) s_bad = 1;
     if (p.zero_tail && !*(volatile int*)&s_fail) {
       const long long end = span == p.nspan - 1 ? p.L : tb + p.span;
       for (long long t = (long long)tb + len + i; t < end; t += kLaT)

@@ -7,6 +7,7 @@
 //
 // Bound by memory: a row is read once into registers, its sums are taken there
 // (the variance about the mean), and its results are written.  All sums are fp32.
+// Forward, 32768 x 1024 fp32 -> bf16: 37 us, 31 at the rate of a plain copy.
 //
 // A row is held by `tpr` threads, thread l with the groups l, l + tpr, ... of VEC
 // elements: lanes of a warp (tpr <= 32, 32 / tpr rows a warp), or a whole CTA.
@@ -263,9 +264,12 @@ template <typename T> struct NormRaw<T, 1> {
 // flight covers the latency of HBM.  The rows stay as they lie in memory and are
 // unpacked twice (for the sums, and for dx), which costs fewer registers than keeping
 // them as fp32.  Measured on B200 (both kernels, us, floor in brackets): 262144 x 128
-// bf16 48 (31), 32768 x 1024 fp32 x 67 (51), 16384 x 4096 fp32 x, bf16 dy 129 (103).
-// One group of 8 a thread: two groups 49 / 78 / 144 us; R = 1 49 / 76 / 141; R = 4
-// spills, 218 at D = 4096; two sets of rows in turn instead of the copy 49 / 74 / 168.
+// bf16 44 (31), 32768 x 1024 fp32 x, bf16 dy 63 (51), 16384 x 4096 the same types 121
+// (103).  Bound by the loads in flight (16 warps of 128 registers a SM), at 128 columns by
+// the issue slots too: single fp32 operations took 45 / 64 / 127.  Not kept: R = 1 at three
+// CTAs a SM 46 / 72 / 137; R = 4 spills, 70 / 105 / 232; two groups of 8 a thread 49 / 78 /
+// 144 when one took 48 / 67 / 129; the rows on their way in shared memory (four stages
+// of cp.async, each thread its own) 45 / 82 / 178.
 template <typename TX, typename TY, int VEC, int G, int R, bool CTA>
 __global__ void __launch_bounds__(CTA ? 512 : kNormThreads, CTA ? 1 : 2)
     pararnn_norm_bwd_kernel(const __grid_constant__ NormParams p) {

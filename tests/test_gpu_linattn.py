@@ -402,3 +402,23 @@ def test_a_state_that_is_not_finite(pr):
     again = pr.scan_linattn(**dict(g, s0=before))
     assert torch.equal(again[0].isnan(), o.isnan()) and torch.equal(again[1].isnan(), s.isnan())
     assert torch.equal(again[0].nan_to_num(), o.nan_to_num())
+
+
+@pytest.mark.parametrize("L", [100, 300, 2000])
+@pytest.mark.parametrize("form", ["recurrent", "chunks"])
+@pytest.mark.parametrize("case", ["lowest", "large"])
+def test_scores_beyond_fp32(pr, form, L, case):
+    """Products q.k that overflow, though no output and no state does: a k of the type's
+    lowest value whose v is zero, and large q and k whose v is small."""
+    x, _ = make(1, L, 3, 3, 3, 3, 64, 64, seed=19, state=False)
+    x["log_decay"] = np.array([-0.01, -0.3, 0.0])
+    t = L - 40
+    if case == "lowest":
+        x["k"][0, t, 1] = float(torch.finfo(BF).min)
+        x["v"][0, t, 1] = 0.0
+    else:
+        x["q"][0, t:, 1] *= 2.0 ** 80
+        x["k"][0, t, 1] *= 2.0 ** 80
+        x["v"][0, t, 1] *= 2.0 ** -90
+    check_scan(pr, x, 0.25, pr.scan_linattn(**on_gpu(x), scale=0.25,
+                                            opts=pr.Options(regime=FORMS[form])))

@@ -306,3 +306,12 @@ def test_outputs_over_inputs_are_refused(fake):  # noqa: F811
     ]
     for call in good:
         call()
+
+
+def test_step_refuses_negative_strides():
+    lib = pr.load()
+    p = ctypes.c_void_p(4096)
+    for name in ("q", "k", "v"):
+        for st in ([-8, 0, 8], [8, 0, -8]):
+            d = _desc(L=1, **{name + "_stride": st})
+            assert lib.pararnn_step_linattn(ctypes.byref(d), p, p, p, 0, p, None, p, p, None) == 1
