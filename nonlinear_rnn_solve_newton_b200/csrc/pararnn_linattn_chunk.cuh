@@ -31,6 +31,19 @@
 // warp of an SM quarter and a third of the issue slots waited for instructions.
 // Every wait is bounded.
 //
+// Measured on B200, heads of 128, bf16: 8 x 4096 tokens of 8 heads 75 us (272 MB, 42 us at
+// the rate of a plain copy), 8 x 8192 of 32 heads 630-770 us (2.2 GB, 334 us).  A chunk
+// takes about 3700 cycles a CTA.  1920 of them are the tensor pipe's (scores 512, update 768,
+// carried 384, local 256: 44% in the counters); DRAM is at 36%, the issue slots at 44%.
+// What is left is the way of one v buffer: load 1150, weigh 1100, the products, read the
+// outputs, stage and store them, load; without any arithmetic of the warps it still takes
+// 66 of 79 us.  The largest runs are held by power besides (990 W, the SM clock at 1.35
+// to 1.4 of 1.965 GHz), whence the spread.  64 state columns a CTA, not 128: 128 fp32
+// states a thread and a third buffer of TMEM do not fit, and half as many CTAs would
+// leave SMs idle at 8 x 8 heads.  Not kept (us at 8 x 8192 x 32 heads, same box): outputs
+// stored by warps of their own 840 against 787; the first copies issued before the
+// rest of the setup 745 against 692; k or v split between the roles: spills.
+//
 // TMEM (512 columns): two buffers of 128 for the scores -- the weighted scores
 // replace the lower half of a buffer, the local output then takes the upper --
 // 192 for the update, 64 for the carried output.
@@ -44,7 +57,8 @@
 //
 // Spans: where (batch row, head, tile) give fewer CTAs than SMs, time is cut into
 // spans.  A first launch (FULL = false) computes the state that each span's own
-// tokens leave, pararnn_linattn_join_kernel carries them over the spans, and the
+// tokens leave (54 us of 155 for 65536 tokens of 12 heads of 64, 67 when one role weighted v
+// and took the update in turn), pararnn_linattn_join_kernel carries them over the spans, and the
 // walk starts each span from the state before it.  In the first launch warps 2-9 weight
 // v, into two places in turn, and the update has two buffers, so that weights, product
 // and state work on three chunks at a time.
@@ -828,7 +842,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 }
 
 // The states that the spans' own tokens leave (s_span, [B, H, spans, dk, dv]) become the
-// states before the spans; the state behind the last one goes to s_out.
+// states before the spans; the state behind the last one goes to s_out.  A thread an
+// element, eight spans' loads on their way at a time.  With eight elements a thread, one
+// load after the other and launches that do not overlap, a scan of 16 spans of 8 heads of
+// 64 took 39 us, so 21.
 constexpr int kLaJoinThreads = 256;
 constexpr int kLaJoinAhead = 8;  // spans whose states are on their way at a time
 
