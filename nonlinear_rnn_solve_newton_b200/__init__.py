@@ -284,10 +284,16 @@ def _device_guard(dev):
     return torch.cuda.device(dev)
 
 
+# the current stream's handle without the object around it (2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream, dev=None):
     """The stream a call is enqueued on: the given one (which must belong to
     the tensors' device) or that device's current stream."""
     if stream is None:
+        if _raw_stream is not None and dev is not None and dev.index is not None:
+            return ctypes.c_void_p(_raw_stream(dev.index))
         s = torch.cuda.current_stream(dev)
     else:
         s = stream
@@ -1031,20 +1037,19 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     B, L, H, Dk, Dv = d.B, d.L, d.H, d.Dk, d.Dv
     _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
     _check_dev("lengths", lengths, torch.int32, (B,))
-    given = out is not None or state_out is not None
-    with _making_on(stream):
-        if out is None:
-            make = torch.empty if lengths is None else torch.zeros
-            out = make((B, L, H, Dv), dtype=torch.bfloat16, device=q.device)
-        if state_out is None:
-            state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
     _check_dev("out", out, torch.bfloat16, (B, L, H, Dv))
     _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
     _check_dev("status", status, torch.int32, (1,))
-    if given:
-        _linattn_apart(d, q, k, v, log_decay, s0, out, state_out, "s0")
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s0=s0, lengths=lengths, out=out,
                       state_out=state_out, status=status)
+    given = out is not None or state_out is not None
+    with _making_on(stream):
+        if out is None:
+            out = (q.new_empty if lengths is None else q.new_zeros)((B, L, H, Dv))
+        if state_out is None:
+            state_out = log_decay.new_empty((B, H, Dk, Dv))
+    if given:
+        _linattn_apart(d, q, k, v, log_decay, s0, out, state_out, "s0")
     nws = _linattn_ws(lib, d, 0)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
@@ -1071,23 +1076,22 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     _check_dev("s0", s0, torch.float32, (B, H, Dk, Dv))
     _check_dev("ds", ds, torch.float32, (B, H, Dk, Dv))
     _check_dev("lengths", lengths, torch.int32, (B,))
+    _check_dev("status", status, torch.int32, (1,))
+    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
+                      status=status)
     if out is None:
         with _making_on(stream):
-            dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device)
-                          for t in (q, k, v))
-            ds0 = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
+            dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(v.shape)
+            ds0 = log_decay.new_empty((B, H, Dk, Dv))
     else:
         dq, dk, dv, ds0 = out
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_dev(name, t, torch.bfloat16, like.shape)
-    _check_dev("ds0", ds0, torch.float32, (B, H, Dk, Dv))
-    _check_dev("status", status, torch.int32, (1,))
-    if out is not None:
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            _check_dev(name, t, torch.bfloat16, like.shape)
+        _check_dev("ds0", ds0, torch.float32, (B, H, Dk, Dv))
+        _one_device(q=q, dq=dq, dk=dk, dv=dv, ds0=ds0)
         _apart((("dq", dq), ("dk", dk), ("dv", dv), ("ds0", ds0)),
                (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("do", do), ("s0", s0),
                 ("ds", ds), ("lengths", lengths)))
-    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
-                      dq=dq, dk=dk, dv=dv, ds0=ds0, status=status)
     nws = _linattn_ws(lib, d, 1)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
@@ -1115,18 +1119,18 @@ def step_linattn(q, k, v, log_decay, s_prev=None, scale=1.0, out=None, state_out
     d = _linattn_desc(q, k, v, log_decay, float(scale), q.dtype)
     B, H, Dk, Dv = d.B, d.H, d.Dk, d.Dv
     _check_dev("s_prev", s_prev, torch.float32, (B, H, Dk, Dv))
+    _check_dev("out", out, q.dtype, (B, H, Dv))
+    _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
+    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s_prev=s_prev, out=out,
+                      state_out=state_out)
     given = out is not None or state_out is not None
     with _making_on(stream):
         if out is None:
-            out = torch.empty((B, H, Dv), dtype=q.dtype, device=q.device)
+            out = q.new_empty((B, H, Dv))
         if state_out is None:
-            state_out = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=q.device)
-    _check_dev("out", out, q.dtype, (B, H, Dv))
-    _check_dev("state_out", state_out, torch.float32, (B, H, Dk, Dv))
+            state_out = log_decay.new_empty((B, H, Dk, Dv))
     if given:
         _linattn_apart(d, q, k, v, log_decay, s_prev, out, state_out, "s_prev")
-    dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, s_prev=s_prev, out=out,
-                      state_out=state_out)
     with _device_guard(dev):
         st = lib.pararnn_step_linattn(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), dt,
                                       _ptr(log_decay), _ptr(s_prev), _ptr(out), _ptr(state_out),
@@ -1187,10 +1191,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, out_dtype=None, st
     y, (mean, rstd) = out, stats or (None, None)
     with _making_on(stream):
         if out is None:
-            y = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+            y = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
         if stats is None:
-            mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-                          for _ in range(2))
+            mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+            rstd = torch.empty_like(mean)
     if out is None and stats is None:
         dev = _one_device(x=x, weight=weight, bias=bias)
     else:
@@ -1224,8 +1228,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, out=None, stream=None):
     _check_dev("rstd", rstd, torch.float32, lead)
     if out is None:
         with _making_on(stream):
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            dw, db = (torch.empty(D, dtype=torch.float32, device=x.device) for _ in range(2))
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+            dw, db = mean.new_empty(D), mean.new_empty(D)
         dev = _one_device(dy=dy, x=x, mean=mean, rstd=rstd, weight=weight)
     else:
         dx, dw, db = out
