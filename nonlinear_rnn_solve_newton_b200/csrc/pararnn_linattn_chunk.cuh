@@ -217,6 +217,11 @@ __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, i
                "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+// A tensor's description on its way into the copies' cache.
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<unsigned long long>(map))
+               : "memory");
+}
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, unsigned src, int x, int y,
                                              int z, int w) {
   asm volatile(
@@ -286,6 +291,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   float* s_out = !FULL ? a.s_span : p.nspan > 1 ? nullptr : a.s_out;
   const long long sr = p.nspan > 1 ? a.dv : a.s_r, sc = p.nspan > 1 ? 1 : a.s_c;
 
+  if (threadIdx.x == 64) {
+    tma_prefetch_map(&tm.k[blockIdx.z]);
+    tma_prefetch_map(&tm.v[blockIdx.z]);
+    if (FULL) tma_prefetch_map(&tm.q[blockIdx.z]);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], FULL ? 2 : 1);
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       if (done < nc) s_fail = 1;
       // no copy is in flight when the CTA exits (only a failed wait leaves loads; a k or
       // v without its q is waited for too, in vain where it was never issued)
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       const long long last = limit < 2000000000LL ? 2000000000LL : limit;
       for (int i = done - 2 < 0 ? 0 : done - 2; i < (done < nc ? done + 1 : done); ++i) {
         la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
@@ -722,12 +732,20 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
     for (int d = 0; d < 16; ++d) s[d] = 0;
     if (s_in && r < a.dk) {
+      const float* sp = s_in + sb + r * sr + cs0 * sc;
+      if (sc == 1) {  // pairs as they lie, waited for where the state is first used
 #pragma unroll
-      for (int d = 0; d < 32; d += 2)
-        if (cs0 + d < a.dv) {
-          const float* sp = s_in + sb + r * sr + (cs0 + d) * sc;
-          s[d / 2] = pair2(sp[0], sp[sc]);
-        }
+        for (int d = 0; d < 32; d += 4)
+          if (cs0 + d < a.dv) {
+            const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(sp + d);
+            s[d / 2] = two.x;
+            s[d / 2 + 1] = two.y;
+          }
+      } else {  // transposed: the lanes' rows are neighbours
+#pragma unroll
+        for (int d = 0; d < 32; d += 2)
+          if (cs0 + d < a.dv) s[d / 2] = pair2(sp[d * sc], sp[(d + 1) * sc]);
+      }
     }
     float ghi, glo;  // gamma^128
     la_two(la_pow(ld, kLaT), ghi, glo);
@@ -825,6 +843,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   }
   if (s_fail) return;
   if (FULL && s_bad) {
+    if (threadIdx.x == 0)  // the outputs stored so far are there before others replace them
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncthreads();
     if (threadIdx.x < kLaAgainThreads)
       la_walk<kLaN, kLaAgainThreads>(
           p, a, b, h, col0, tb, len, s_in ? s_in + sb : nullptr, sr, sc,
