@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tma_prefetch_map(&tm.k[blockIdx.z]);
     tma_prefetch_map(&tm.v[blockIdx.z]);
     if (FULL) tma_prefetch_map(&tm.q[blockIdx.z]);
+    if (FULL && !(BWD && a.o_f32)) tma_prefetch_map(&tm.o[blockIdx.z]);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -850,15 +851,27 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       la_walk<kLaN, kLaAgainThreads>(
           p, a, b, h, col0, tb, len, s_in ? s_in + sb : nullptr, sr, sc,
           s_out ? s_out + sb : nullptr, *reinterpret_cast<LaWalkSmem<kLaN>*>(dsmem));
-  } else if (warp >= 10 && s_out && row < a.dk) {
+  } else if (warp >= 10 && s_out) {
+    // through shared memory (nothing uses q's place any more), so that 16 lanes store one
+    // row: stored straight from the rows' threads, 128 x 64 states took 3100 cycles
 #pragma unroll
-    for (int d = 0; d < 32; d += 4)
-      if (cs0 + d < a.dv) {
-        float4 x;
-        unpair2(s[d / 2], x.x, x.y);
-        unpair2(s[d / 2 + 1], x.z, x.w);
-        *reinterpret_cast<float4*>(s_out + sb + (long long)row * a.dv + cs0 + d) = x;
-      }
+    for (int d = 0; d < 32; d += 4) {
+      float4 x;
+      unpair2(s[d / 2], x.x, x.y);
+      unpair2(s[d / 2 + 1], x.z, x.w);
+      if (KD == 128 || row < KD)
+        sts128(sbase + Sm::kQ + row * 256 + (((8 * hf + d / 4) ^ (row & 15)) << 4),
+               __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
+               __float_as_uint(x.w));
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < KD / 16; ++i) {
+      const int at = (int)threadIdx.x - 320 + 256 * i, to = at >> 4, u = at & 15;
+      if (to < a.dk && col0 + 4 * u < a.dv)
+        *reinterpret_cast<uint4*>(s_out + sb + (long long)to * a.dv + col0 + 4 * u) =
+            lds128(sbase + Sm::kQ + to * 256 + ((u ^ (to & 15)) << 4));
+    }
   }
 }
 
