@@ -150,8 +150,8 @@ pararnn_status_t la_walks(const LaParams& lp, const LaMaps& tm, cudaStream_t st)
 // The form of a call and, for the chunked form, the spans that time is cut into.
 // The recurrent form's time grows with every token, the chunked one's with every 128.
 // Scan, one launch in a graph, recurrent / chunked: one sequence of 8 heads of 128 at 8
-// tokens 8.8 / 9.9 us, at 16 14.2 / 9.9; 8 x 16 heads of 128 at 8 tokens 14.1 / 19.1, at
-// 16 23.6 / 18.9; 32 x 16 heads of 64 at 8 tokens 16.9 / 30.9, at 16 27.3 / 30.8.
+// tokens 8.7 / 8.4 us, at 16 14.2 / 8.6; 8 x 16 heads of 128 at 8 tokens 14.2 / 16.9, at
+// 16 23.9 / 16.8; 32 x 16 heads of 64 at 8 tokens 17.0 / 29.2, at 16 27.9 / 29.2.
 constexpr long long kLaRecurrentMax = 8;
 constexpr long long kLaSms = 148;  // one CTA of the chunked form each
 
@@ -172,8 +172,8 @@ LaPlan la_plan(const pararnn_linattn_t* d, bool backward, const pararnn_options_
   // In units of one chunk's walk (2 us): a CTA takes about two to start and end.  With more
   // than one span the states are walked first, 0.45 a chunk, and the join and two more
   // launches take 4 to 7.  Measured in us, one span and the best number of them: 2048 tokens of
-  // 8 heads of 64 38.3, 20.5 (16 spans); 4096 of 16 heads of 128 67.7, 45.5 (4); 65536 of
-  // 12 heads of 64 1014, 149 (12); 4 x 4096 of 8 heads of 128 69.8, 76.7 (2: not taken).
+  // 8 heads of 64 38, 18 (16 spans); 4096 of 16 heads of 128 68, 46 (4); 65536 of 12
+  // heads of 64 1014, 149 (12); 4 x 4096 of 8 heads of 128 70, 77 (2: not taken).
   const double join = d->Dk * d->Dv <= 64 * 64 ? 4.0 : 7.0;
   double best = 0.0;
   for (long long want = 1; want <= chunks && (want - 1) * items <= 2 * kLaSms; ++want) {
