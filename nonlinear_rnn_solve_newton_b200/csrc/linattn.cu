@@ -449,7 +449,7 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   a.c_kv = 1.0f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // tiles of 4096 elements, 4 rows a thread: 128 rows x 32 columns, or 64 x 64 (with 32
-  // columns half of the threads would have no rows: 256 x 32 states of 64 x 64 76 us)
+  // columns half of the threads would have no rows: 256 x 32 states of 64 x 64 76 us, so 46)
   const bool low = d->Dk <= 64;
   const long long cols = low ? 64 : 32, grid = d->B * d->H * ((d->Dv + cols - 1) / cols);
   if (grid >= (1LL << 31)) return PARARNN_ERR_INVALID_ARGUMENT;

@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pararnn_sm100.cuh"
+
 namespace pararnn {
 
 constexpr int kLaMaxDim = 128;   // largest Dk and Dv
@@ -252,7 +254,8 @@ __global__ void __launch_bounds__(kLaRecThreads)
 // thread, all of whose loads are issued before anything is waited for; the small
 // vectors come straight from global memory.  In place is fine: each element is read
 // and written by the same thread.  Measured on B200 at 192 x 32 states of 128 x 128 (the
-// floor is 123 us): tiles of 32 columns 143 us, whole rows of 128 (16 rows a thread) 158.
+// floor is 124 us): tiles of 32 columns on pairs of fp32 131 us; on single ones 155, and
+// 143 with gamma as one float; whole rows of 128 (16 rows a thread, as the 143) 158.
 constexpr int kLaStepThreads = 256;
 
 template <typename T, int COLS, int ROWS>
@@ -268,19 +271,22 @@ __global__ void __launch_bounds__(kLaStepThreads)
   const int cg = lane % CG, rg = (int)threadIdx.x / CG, col = c0 + cg * 4;
   const bool cok = col < a.dv;
   const long long sb = (long long)bh * a.dk * a.dv;
-  float4 s[R];
+  ulonglong2 s[R];  // two pairs of neighbouring columns
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = r * RG + rg;
-    s[r] = a.s_in && cok && row < a.dk
-               ? __ldcs(reinterpret_cast<const float4*>(a.s_in + sb + row * a.dv + col))
-               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    s[r] = make_ulonglong2(0ull, 0ull);
+    if (a.s_in && cok && row < a.dk)
+      s[r] = __ldcs(reinterpret_cast<const ulonglong2*>(a.s_in + sb + row * a.dv + col));
   }
   const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
   const T* k = static_cast<const T*>(a.k.p) + b * a.k.sb + (h / a.k.rep) * a.k.sh;
   const T* v = static_cast<const T*>(a.v.p) + b * a.v.sb + (h / a.v.rep) * a.v.sh;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (cok) x = make_float4(la_load(v + col), la_load(v + col + 1), la_load(v + col + 2), la_load(v + col + 3));
+  f32x2 x0 = 0, x1 = 0;
+  if (cok) {
+    x0 = pair2(la_load(v + col), la_load(v + col + 1));
+    x1 = pair2(la_load(v + col + 2), la_load(v + col + 3));
+  }
   float kk[R], qq[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -288,17 +294,35 @@ __global__ void __launch_bounds__(kLaStepThreads)
     kk[r] = row < a.dk ? la_load(k + row) : 0.0f;
     qq[r] = row < a.dk ? la_load(q + row) : 0.0f;
   }
-  const float gamma = expf(p.log_decay[h]);
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // a slow head's gamma as two floats: the half step that one leaves would add up over its
+  // thousands of tokens.  1 + expm1 is off by 2^-23 |1 - gamma|, which over the
+  // 1 / |1 - gamma| tokens of its memory is one rounding; a fast head forgets sooner.
+  // (exp in 64 bits by one thread and a barrier took 166 us where this took 155)
+  const float ld = p.log_decay[h];
+  float gamma, glow = 0.0f;
+  if (fabsf(ld) < 0.25f) {
+    const float less = expm1f(ld);
+    gamma = 1.0f + less;
+    glow = less - (gamma - 1.0f);
+  } else {
+    gamma = expf(ld);
+  }
+  const f32x2 g2 = pair2(gamma, gamma), l2 = pair2(glow, glow);
+  f32x2 o0 = 0, o1 = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = r * RG + rg;
-    const float4 w = make_float4(fmaf(kk[r], x.x, gamma * s[r].x), fmaf(kk[r], x.y, gamma * s[r].y),
-                                 fmaf(kk[r], x.z, gamma * s[r].z), fmaf(kk[r], x.w, gamma * s[r].w));
-    o = make_float4(fmaf(qq[r], w.x, o.x), fmaf(qq[r], w.y, o.y), fmaf(qq[r], w.z, o.z),
-                    fmaf(qq[r], w.w, o.w));
-    if (cok && row < a.dk) *reinterpret_cast<float4*>(a.s_out + sb + row * a.dv + col) = w;
+    const f32x2 k2 = pair2(kk[r], kk[r]), q2 = pair2(qq[r], qq[r]);
+    const f32x2 w0 = fma2(k2, x0, fma2(g2, s[r].x, mul2(l2, s[r].x))),
+                w1 = fma2(k2, x1, fma2(g2, s[r].y, mul2(l2, s[r].y)));
+    o0 = fma2(q2, w0, o0);
+    o1 = fma2(q2, w1, o1);
+    if (cok && row < a.dk)
+      *reinterpret_cast<ulonglong2*>(a.s_out + sb + row * a.dv + col) = make_ulonglong2(w0, w1);
   }
+  float4 o;
+  unpair2(o0, o.x, o.y);
+  unpair2(o1, o.z, o.w);
 #pragma unroll
   for (int m = CG; m < 32; m <<= 1) {
     o.x += __shfl_xor_sync(0xffffffffu, o.x, m);

@@ -422,3 +422,27 @@ def test_scores_beyond_fp32(pr, form, L, case):
         x["v"][0, t, 1] *= 2.0 ** -90
     check_scan(pr, x, 0.25, pr.scan_linattn(**on_gpu(x), scale=0.25,
                                             opts=pr.Options(regime=FORMS[form])))
+
+
+def test_many_steps_keep_the_state(pr):
+    """Thousands of decode steps with slow decays: what each rounds must not add up in
+    one direction.  A step rounds gamma s + k v twice (2^-24 each); over the 3000 steps of
+    the walk independent roundings give at most 2^-24 (2 x 3000)^(1/2) = 2^-17.7 of the
+    state's size, while the half step that gamma as one float leaves, 2^-25 a token, would
+    be 3000 of them, 2^-13.4."""
+    H, D, n = 6, 64, 3000
+    rng = np.random.default_rng(20)
+    lam = np.float32([-1e-4, -2.3e-4, -3.7e-5, -5.1e-4, -7e-5, -1.3e-5]).astype(float)
+    s = rng.standard_normal((1, H, D, D)).astype(np.float32)
+    want = s.astype(np.float64)
+    k, v = (ref.bf16(rng.standard_normal((n, 1, H, D))) for _ in range(2))
+    q = dev(k[0], BF)
+    got, gk, gv, g = dev(s), dev(k, BF), dev(v, BF), dev(lam)
+    gamma = np.exp(lam)[:, None, None]
+    for t in range(n):
+        pr.step_linattn(q, gk[t], gv[t], g, got, state_out=got)
+        want = gamma * want + k[t][..., :, None] * v[t][..., None, :]
+    for h in range(H):
+        a, b = got[0, h].double().cpu().numpy(), want[0, h]
+        assert np.linalg.norm(a - b) <= 2.0 ** -17 * np.linalg.norm(b), (
+            h, np.linalg.norm(a - b) / np.linalg.norm(b))
