@@ -7,7 +7,8 @@
 //
 // Bound by memory: a row is read once into registers, its sums are taken there
 // (the variance about the mean), and its results are written.  All sums are fp32.
-// Forward, 32768 x 1024 fp32 -> bf16: 37 us, 31 at the rate of a plain copy.
+// Forward, on pairs of fp32: 32768 x 1024 fp32 -> bf16 37 us (31 at the rate of a plain
+// copy), 262144 x 128 bf16 26 us (21; on single fp32 33: bound by the issue slots then).
 //
 // A row is held by `tpr` threads, thread l with the groups l, l + tpr, ... of VEC
 // elements: lanes of a warp (tpr <= 32, 32 / tpr rows a warp), or a whole CTA.
@@ -131,66 +132,6 @@ __device__ __forceinline__ void norm_sum(float* v, int tpr, float (*sm)[2][N], i
   }
 }
 
-template <typename TX, typename TY, int VEC, int G, bool CTA>
-__global__ void __launch_bounds__(CTA ? 512 : kNormThreads)
-    pararnn_norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float sm[CTA ? 16 : 1][2][1];
-  const int lane = threadIdx.x & 31;
-  const int l = CTA ? (int)threadIdx.x : lane % p.tpr;
-  const long long row = CTA ? (long long)blockIdx.x
-                            : (blockIdx.x * (long long)(kNormThreads / 32) + (threadIdx.x >> 5)) *
-                                      (32 / p.tpr) + lane / p.tpr;
-  const bool live = row < p.M;  // the same for every thread of a row
-  const int ng = p.D / VEC;
-  const TX* x = static_cast<const TX*>(p.x) + row * p.sx;
-  float v[G][VEC], s[1] = {0.0f};
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int at = l + g * p.tpr;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[g][i] = 0.0f;
-    if (live && at < ng) norm_load<VEC>(x + at * VEC, v[g]);
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) s[0] += v[g][i];
-  }
-  norm_sum<1, CTA>(s, p.tpr, sm, 0);
-  const float mean = s[0] / (float)p.D;
-  s[0] = 0.0f;
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    if (l + g * p.tpr < ng) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        v[g][i] -= mean;
-        s[0] = fmaf(v[g][i], v[g][i], s[0]);
-      }
-    }
-  }
-  norm_sum<1, CTA>(s, p.tpr, sm, 1);
-  const float rstd = 1.0f / sqrtf(s[0] / (float)p.D + p.eps);
-  if (!live) return;
-  TY* y = static_cast<TY*>(p.y) + row * p.D;
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int at = (l + g * p.tpr) * VEC;
-    if (at < p.D) {
-      float w[VEC], b[VEC];
-      norm_weight<VEC>(p.w, at, 1.0f, w);
-      norm_weight<VEC>(p.b, at, 0.0f, b);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) v[g][i] = fmaf(v[g][i] * rstd, w[i], b[i]);
-      norm_store<VEC>(y + at, v[g]);
-    }
-  }
-  if (l == 0) {
-    p.mean[row] = mean;
-    p.rstd[row] = rstd;
-  }
-}
-
 // A group's elements as the arithmetic takes them: four pairs, or one number.
 template <int VEC> struct NormVal;
 template <> struct NormVal<8> {
@@ -259,6 +200,81 @@ template <typename T> struct NormRaw<T, 1> {
   __device__ __forceinline__ void zero() { a = 0.0f; }
   __device__ __forceinline__ void get(float* v) const { v[0] = a; }
 };
+
+template <typename TX, typename TY, int VEC, int G, bool CTA>
+__global__ void __launch_bounds__(CTA ? 512 : kNormThreads)
+    pararnn_norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float sm[CTA ? 16 : 1][2][1];
+  const int lane = threadIdx.x & 31;
+  const int l = CTA ? (int)threadIdx.x : lane % p.tpr;
+  const long long row = CTA ? (long long)blockIdx.x
+                            : (blockIdx.x * (long long)(kNormThreads / 32) + (threadIdx.x >> 5)) *
+                                      (32 / p.tpr) + lane / p.tpr;
+  const bool live = row < p.M;  // the same for every thread of a row
+  const int ng = p.D / VEC;
+  const TX* x = static_cast<const TX*>(p.x) + row * p.sx;
+  using V = NormVal<VEC>;
+  using T = typename V::T;
+  constexpr int N = V::N;
+  T v[G][N], sum;
+  float s[1];
+  nset(sum, 0.0f);
+  NormRaw<TX, VEC> raw[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int at = l + g * p.tpr;
+    raw[g].zero();
+    if (live && at < ng) raw[g].load(x + at * VEC);
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    raw[g].get(v[g]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum = nadd(sum, v[g][i]);
+  }
+  s[0] = nsum(sum);
+  norm_sum<1, CTA>(s, p.tpr, sm, 0);
+  const float mean = s[0] / (float)p.D;
+  T minus;
+  nset(minus, -mean);
+  nset(sum, 0.0f);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (l + g * p.tpr < ng) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[g][i] = nadd(v[g][i], minus);
+        sum = nfma(v[g][i], v[g][i], sum);
+      }
+    }
+  }
+  s[0] = nsum(sum);
+  norm_sum<1, CTA>(s, p.tpr, sm, 1);
+  const float rstd = 1.0f / sqrtf(s[0] / (float)p.D + p.eps);
+  if (!live) return;
+  TY* y = static_cast<TY*>(p.y) + row * p.D;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int at = (l + g * p.tpr) * VEC;
+    if (at < p.D) {
+      float w[VEC], b[VEC], out[VEC];
+      T w2[N], b2[N], rs;
+      norm_weight<VEC>(p.w, at, 1.0f, w);
+      norm_weight<VEC>(p.b, at, 0.0f, b);
+      nput(w, w2);
+      nput(b, b2);
+      nset(rs, rstd);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[g][i] = nfma(nmul(v[g][i], rs), w2[i], b2[i]);
+      nget(v[g], out);
+      norm_store<VEC>(y + at, out);
+    }
+  }
+  if (l == 0) {
+    p.mean[row] = mean;
+    p.rstd[row] = rstd;
+  }
+}
 
 // R rows at a time, and the next R on their way while these are worked on: what is in
 // flight covers the latency of HBM.  The rows stay as they lie in memory and are
