@@ -128,10 +128,7 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
     pararnn_norm_long_dx_kernel<TX, TY><<<(unsigned)np.M, 1024, 0, st>>>(np);
     pararnn_norm_long_dw_kernel<TX, TY>
         <<<dim3((unsigned)((np.D + 127) / 128), (unsigned)np.nparts), 128, 0, st>>>(np);
-    norm_join(np, st);
-    return;
-  }
-  if (vec) {
+  } else if (vec) {
     if (sh.groups == 4)
       norm_bwd_go<TX, TY, 8, 4, 1>(np, sh, st);
     else if (sh.groups == 2)
@@ -141,8 +138,8 @@ void norm_bwd(NormParams& np, bool vec, cudaStream_t st) {
   } else {
     norm_bwd_go<TX, TY, 1, 16, 1>(np, sh, st);
   }
-  if (np.nparts > 1)
-    norm_join(np, st);
+  // one part went straight to dweight and dbias; a single row has no workspace
+  if (np.nparts > 1) norm_join(np, st);
 }
 
 }  // namespace

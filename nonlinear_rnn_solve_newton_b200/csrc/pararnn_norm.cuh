@@ -600,8 +600,13 @@ __global__ void __launch_bounds__(128)
     sw = fmaf(g[0], (v[0] - p.mean[r]) * p.rstd[r], sw);
     sb += g[0];
   }
-  p.part[(long long)blockIdx.y * p.D + d] = sw;
-  p.part[(long long)(p.nparts + blockIdx.y) * p.D + d] = sb;
+  if (p.nparts > 1) {
+    p.part[(long long)blockIdx.y * p.D + d] = sw;
+    p.part[(long long)(p.nparts + blockIdx.y) * p.D + d] = sb;
+  } else {  // one slice: its sums are the result, and there is no workspace
+    p.dw[d] = sw;
+    p.db[d] = sb;
+  }
 }
 
 }  // namespace pararnn

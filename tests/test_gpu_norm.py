@@ -198,3 +198,21 @@ def test_streams_and_graph(pr):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(want, outs))
+
+
+@pytest.mark.parametrize("ty", [F32, BF])
+@pytest.mark.parametrize("tx", [F32, BF])
+@pytest.mark.parametrize("D,off", [(8193, 0), (16392, 0), (20011, 0), (8200, 1)])
+def test_one_row_longer_than_registers(pr, D, off, tx, ty):
+    """One row needs no workspace, however long: its sums go straight to the results."""
+    x, w, b, rng = make(1, D, 26, tx)
+    assert pr.load().pararnn_layer_norm_workspace_size(1, D) == 256
+    wide = torch.zeros(1, D + off, dtype=tx, device="cuda")
+    X = wide[:, off:]                    # off = 1: not on 16 bytes, an element an access
+    X.copy_(dev(x, tx))
+    got = pr.layer_norm(X, dev(w), dev(b), out_dtype=ty)
+    check_forward(x, w, b, got, ty)
+    dy = rng.standard_normal((1, D))
+    dy = ref.bf16(dy) if ty == BF else dy.astype(np.float32).astype(float)
+    grads = pr.layer_norm_backward(dev(dy, ty), X, got[1], got[2], dev(w))
+    check_backward(dy, x, host(got[1]), host(got[2]), w, grads, tx)
