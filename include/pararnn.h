@@ -512,7 +512,8 @@ pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* desc, const void*
  * solves give fp32 h, the projections read bf16 x) and, on rows of one head,
  * behind linear attention (the pages have no counterpart).
  *   y = (x - mean) rstd weight + bias,  rstd = (var + eps)^(-1/2)
- *  x [M, D] fp32 or bf16, rows x_stride elements apart (last axis contiguous);
+ *  x [M, D] fp32 or bf16, rows x_stride elements apart (last axis contiguous), M below
+ *  2^31 and D up to 2^30;
  *  weight, bias [D] fp32 or NULL (1 and 0);  y [M, D] fp32 or bf16, contiguous;
  *  mean, rstd [M] fp32: the rows' statistics, which the backward pass reads.
  *  Outputs (here and below) must not overlap inputs or each other.

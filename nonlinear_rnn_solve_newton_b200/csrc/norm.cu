@@ -13,8 +13,11 @@ namespace {
 
 constexpr int kNormSms = 148;
 
+// Columns are counted in int, and a thread's next column is up to 1024 beyond the row.
+constexpr int64_t kNormMaxCols = 1LL << 30;
+
 bool norm_sizes_ok(int64_t M, int64_t D) {
-  return M >= 0 && D > 0 && D < (1LL << 31) && M < (1LL << 31) && M < (1LL << 62) / D;
+  return M >= 0 && D > 0 && D <= kNormMaxCols && M < (1LL << 31);
 }
 
 bool norm_aligned(const void* p, pararnn_dtype_t t) {

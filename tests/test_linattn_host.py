@@ -315,3 +315,17 @@ def test_step_refuses_negative_strides():
         for st in ([-8, 0, 8], [8, 0, -8]):
             d = _desc(L=1, **{name + "_stride": st})
             assert lib.pararnn_step_linattn(ctypes.byref(d), p, p, p, 0, p, None, p, p, None) == 1
+
+
+def test_layer_norm_refuses_rows_beyond_its_counters():
+    # a column index is an int and runs up to 1024 beyond the row before it is compared:
+    # rows of nearly 2^31 columns would wrap to negative offsets
+    lib = pr.load()
+    p = ctypes.c_void_p(4096)
+    for D in ((1 << 31) - 1, (1 << 31) - 512, (1 << 30) + 8):
+        assert lib.pararnn_layer_norm_workspace_size(2, D) == 0
+        assert lib.pararnn_layer_norm(p, 0, D, None, None, p, 0, p, p, 0, D, 1e-5, None) == 1
+        assert lib.pararnn_layer_norm_backward(p, 0, D, p, 0, D, None, p, p, p, p, p, 0, D,
+                                               None, 0, None) == 1
+    assert lib.pararnn_layer_norm_workspace_size(2, 1 << 30) > 0
+    assert lib.pararnn_layer_norm(p, 0, 8, None, None, p, 0, p, p, 0, 1 << 30, 1e-5, None) == 0
