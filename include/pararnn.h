@@ -434,6 +434,7 @@ pararnn_status_t pararnn_probe_rate(int32_t pipe, int32_t iters, float* sink, in
  *   S_t = gamma_h S_{t-1} + k_t^T v_t,  o_t = scale q_t S_t,  t = 1..n_b,
  *   gamma_h = exp(log_decay[h]),  n_b = min(max(lengths[b], 0), L) or L.
  * A log decay of -inf is gamma = 0 (each token sees itself only), 0 is gamma = 1.
+ * An infinite state stays infinite, however small gamma is, unless gamma = 0 (0 inf = NaN).
  *
  * Shapes of a call (host struct):
  *  B, L       : batch rows and tokens.     H : heads (decays, states, outputs).

@@ -214,6 +214,21 @@ pararnn_status_t la_launch(LaParams& lp, const LaPlan& pl, float* span_ws,
   return dk <= 64 ? la_walks<64>(lp, tm, st) : la_walks<128>(lp, tm, st);
 }
 
+// Tiles of 4096 elements, 4 rows a thread: 128 rows x 32 columns, or 64 x 64 (with 32
+// columns half of the threads would have no rows: 256 x 32 states of 64 x 64 76 us, so 45).
+template <typename T>
+void la_launch_step(const LaParams& lp, unsigned grid, cudaStream_t st) {
+  const int dk = lp.pass[0].dk;
+  if (dk == 128)
+    pararnn_linattn_step_kernel<T, 32, 128, false><<<grid, kLaStepThreads, 0, st>>>(lp);
+  else if (dk > 64)
+    pararnn_linattn_step_kernel<T, 32, 128, true><<<grid, kLaStepThreads, 0, st>>>(lp);
+  else if (dk == 64)
+    pararnn_linattn_step_kernel<T, 64, 64, false><<<grid, kLaStepThreads, 0, st>>>(lp);
+  else
+    pararnn_linattn_step_kernel<T, 64, 64, true><<<grid, kLaStepThreads, 0, st>>>(lp);
+}
+
 // Workspace: fp32 per-head gradients of the streams whose heads are shared, and
 // the spans' states of every pass.
 constexpr size_t kLaNoWs = 256;  // what the size says where a call needs none
@@ -448,20 +463,11 @@ extern "C" pararnn_status_t pararnn_step_linattn(const pararnn_linattn_t* d, con
   a.c_out = d->scale;
   a.c_kv = 1.0f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // tiles of 4096 elements, 4 rows a thread: 128 rows x 32 columns, or 64 x 64 (with 32
-  // columns half of the threads would have no rows: 256 x 32 states of 64 x 64 76 us, so 46)
-  const bool low = d->Dk <= 64;
-  const long long cols = low ? 64 : 32, grid = d->B * d->H * ((d->Dv + cols - 1) / cols);
+  const long long cols = d->Dk <= 64 ? 64 : 32, grid = d->B * d->H * ((d->Dv + cols - 1) / cols);
   if (grid >= (1LL << 31)) return PARARNN_ERR_INVALID_ARGUMENT;
-  const bool bf16 = dtype == PARARNN_BF16;
-  const dim3 g((unsigned)grid);
-  if (bf16 && low)
-    pararnn_linattn_step_kernel<__nv_bfloat16, 64, 64><<<g, kLaStepThreads, 0, st>>>(lp);
-  else if (bf16)
-    pararnn_linattn_step_kernel<__nv_bfloat16, 32, 128><<<g, kLaStepThreads, 0, st>>>(lp);
-  else if (low)
-    pararnn_linattn_step_kernel<float, 64, 64><<<g, kLaStepThreads, 0, st>>>(lp);
+  if (dtype == PARARNN_BF16)
+    la_launch_step<__nv_bfloat16>(lp, (unsigned)grid, st);
   else
-    pararnn_linattn_step_kernel<float, 32, 128><<<g, kLaStepThreads, 0, st>>>(lp);
+    la_launch_step<float>(lp, (unsigned)grid, st);
   return cudaGetLastError() == cudaSuccess ? PARARNN_OK : PARARNN_ERR_CUDA;
 }

@@ -78,17 +78,26 @@ __device__ __forceinline__ long long la_span_tokens(const LaParams& p, int b, in
   return n < 0 ? 0 : (p.nspan > 1 && n > p.span ? p.span : n);
 }
 
-// x = hi + lo with hi the nearest float (0 beyond the range of a float)
-__device__ __forceinline__ void la_two(double x, float& hi, float& lo) {
-  hi = (float)x;
-  lo = isfinite(hi) ? (float)(x - (double)hi) : 0.0f;
-}
-
 // gamma^i in 64 bits; gamma^0 = 1 also for gamma = 0
 __device__ __noinline__ inline double la_powl(float log_decay, long long i) {
   return i == 0 ? 1.0 : exp((double)log_decay * (double)i);
 }
 __device__ __forceinline__ double la_pow(float log_decay, int i) { return la_powl(log_decay, i); }
+
+// gamma^i = hi + lo, i > 0, with hi rounded towards zero.  Where gamma is not zero neither hi
+// nor lo is, and neither is negative: hi x + lo x keeps an infinite x as the recurrence does
+// (0 inf or inf - inf would be NaN).  The least value, 2^-149, is far below every rounding of a
+// normal hi; a smaller gamma^i becomes twice that.
+constexpr float kLaLeast = 1.40129846e-45f;
+__device__ __forceinline__ void la_two(float log_decay, long long i, float& hi, float& lo) {
+  const double x = la_powl(log_decay, i);
+  hi = __double2float_rz(x);
+  lo = (float)(x - (double)hi);
+  if (log_decay > -INFINITY) {
+    hi = fmaxf(hi, kLaLeast);
+    lo = fmaxf(lo, kLaLeast);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // Recurrent form.  THREADS threads hold a COLS-column tile of one (b, h) state in
@@ -128,7 +137,7 @@ __device__ __noinline__ void la_walk(const LaParams& p, const LaPass& a, int b, 
   // of times, and the half step that one float leaves (2^-25 near 1) would add up
   // in the same direction every time
   float gamma, glow;
-  la_two(la_pow(p.log_decay[h], 1), gamma, glow);
+  la_two(p.log_decay[h], 1, gamma, glow);
 
   float s[R][4];
 #pragma unroll
@@ -254,12 +263,15 @@ __global__ void __launch_bounds__(kLaRecThreads)
 // thread, all of whose loads are issued before anything is waited for; the small
 // vectors come straight from global memory.  In place is fine: each element is read
 // and written by the same thread.  Measured on B200 at 192 x 32 states of 128 x 128 (the
-// floor is 124 us): tiles of 32 columns on pairs of fp32 131 us; on single ones 155, and
+// floor is 124 us): tiles of 32 columns on pairs of fp32 130 us; on single ones 155, and
 // 143 with gamma as one float; whole rows of 128 (16 rows a thread, as the 143) 158.
 constexpr int kLaStepThreads = 256;
 
-template <typename T, int COLS, int ROWS>
-__global__ void __launch_bounds__(kLaStepThreads)
+// PART: fewer than ROWS rows, each asked for.  With those conditions where all rows are there
+// 256 x 32 states of 64 x 64 take 49 us, without 45; 192 x 32 of 96 x 96 take 93 either way.
+// Six CTAs a SM (40 registers; five that take 48: 131 and 47 us at 128 and 64).
+template <typename T, int COLS, int ROWS, bool PART>
+__global__ void __launch_bounds__(kLaStepThreads, 6)
     pararnn_linattn_step_kernel(const __grid_constant__ LaParams p) {
   constexpr int CG = COLS / 4, RG = kLaStepThreads / CG, R = ROWS / RG;
   __shared__ float4 s_part[kLaStepThreads / 32][CG];
@@ -276,7 +288,7 @@ __global__ void __launch_bounds__(kLaStepThreads)
   for (int r = 0; r < R; ++r) {
     const int row = r * RG + rg;
     s[r] = make_ulonglong2(0ull, 0ull);
-    if (a.s_in && cok && row < a.dk)
+    if (a.s_in && cok && (!PART || row < a.dk))
       s[r] = __ldcs(reinterpret_cast<const ulonglong2*>(a.s_in + sb + row * a.dv + col));
   }
   const T* q = static_cast<const T*>(a.q.p) + b * a.q.sb + (h / a.q.rep) * a.q.sh;
@@ -291,21 +303,26 @@ __global__ void __launch_bounds__(kLaStepThreads)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = r * RG + rg;
-    kk[r] = row < a.dk ? la_load(k + row) : 0.0f;
-    qq[r] = row < a.dk ? la_load(q + row) : 0.0f;
+    kk[r] = !PART || row < a.dk ? la_load(k + row) : 0.0f;
+    qq[r] = !PART || row < a.dk ? la_load(q + row) : 0.0f;
   }
   // a slow head's gamma as two floats: the half step that one leaves would add up over its
-  // thousands of tokens.  1 + expm1 is off by 2^-23 |1 - gamma|, which over the
-  // 1 / |1 - gamma| tokens of its memory is one rounding; a fast head forgets sooner.
+  // thousands of tokens.  1 + expm1 is off by 2^-23 |1 - gamma| and 2^-49; the first, over the
+  // 1 / |1 - gamma| tokens of its memory, is one rounding; a fast head forgets sooner.
+  // Both as in la_two: not negative, and zero only for gamma = 0, for infinite states.
   // (exp in 64 bits by one thread and a barrier took 166 us where this took 155)
   const float ld = p.log_decay[h];
   float gamma, glow = 0.0f;
   if (fabsf(ld) < 0.25f) {
     const float less = expm1f(ld);
-    gamma = 1.0f + less;
+    gamma = __fadd_rz(1.0f, less);
     glow = less - (gamma - 1.0f);
   } else {
     gamma = expf(ld);
+  }
+  if (ld > -INFINITY) {
+    gamma = fmaxf(gamma, kLaLeast);
+    glow = fmaxf(glow, kLaLeast);
   }
   const f32x2 g2 = pair2(gamma, gamma), l2 = pair2(glow, glow);
   f32x2 o0 = 0, o1 = 0;
@@ -315,10 +332,12 @@ __global__ void __launch_bounds__(kLaStepThreads)
     const f32x2 k2 = pair2(kk[r], kk[r]), q2 = pair2(qq[r], qq[r]);
     const f32x2 w0 = fma2(k2, x0, fma2(g2, s[r].x, mul2(l2, s[r].x))),
                 w1 = fma2(k2, x1, fma2(g2, s[r].y, mul2(l2, s[r].y)));
-    o0 = fma2(q2, w0, o0);
-    o1 = fma2(q2, w1, o1);
-    if (cok && row < a.dk)
-      *reinterpret_cast<ulonglong2*>(a.s_out + sb + row * a.dv + col) = make_ulonglong2(w0, w1);
+    if (!PART || row < a.dk) {  // a row that is not there would make 0 inf of an infinite v
+      o0 = fma2(q2, w0, o0);
+      o1 = fma2(q2, w1, o1);
+      if (cok)
+        *reinterpret_cast<ulonglong2*>(a.s_out + sb + row * a.dv + col) = make_ulonglong2(w0, w1);
+    }
   }
   float4 o;
   unpair2(o0, o.x, o.y);

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
     }
     float ghi, glo;  // gamma^128
-    la_two(la_pow(ld, kLaT), ghi, glo);
+    la_two(ld, kLaT, ghi, glo);
     const float vfull = FULL ? weight(kLaT) : 0.0f, vtail = FULL ? weight(n_tail) : 0.0f;
     bool ok = true;
     for (int c = 0; c <= nc; ++c) {
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         tc_fence_after();
         float h1 = ghi, h2 = glo;
         const int m = rows(c - 1);
-        if (m < kLaT) la_two(la_pow(ld, m), h1, h2);
+        if (m < kLaT) la_two(ld, m, h1, h2);
         const f32x2 hh1 = pair2(h1, h1), hh2 = pair2(h2, h2);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     }
     if (!ok) {
       s_fail = 1;
-    } else if (FULL && r < a.dk) {
+    } else if (r < a.dk) {
       bool fine = true;
 #pragma unroll
       for (int d = 0; d < 16; ++d) {
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
                  : "memory");
   }
   if (s_fail) return;
-  if (FULL && s_bad) {
+  if (s_bad) {  // the outputs of a walk of the states only are replaced by the full one's
     if (threadIdx.x == 0)  // the outputs stored so far are there before others replace them
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncthreads();
@@ -890,7 +890,7 @@ __global__ void __launch_bounds__(kLaJoinThreads)
   const float ld = p.log_decay[bh % p.H];
   const int n = a.dk * a.dv, e = (int)(threadIdx.x + blockIdx.y * kLaJoinThreads);
   float ghi, glo;  // of a whole span
-  la_two(la_powl(ld, p.span), ghi, glo);
+  la_two(ld, p.span, ghi, glo);
   wait_for_launch_before();
   if (e >= n) return;
   const int r = e / a.dv, c = e % a.dv;
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kLaJoinThreads)
       const int g = a.rev ? p.nspan - 1 - k0 - i : k0 + i;
       const long long m = la_span_tokens(p, b, g);
       float h1 = ghi, h2 = glo;
-      if (m != p.span) la_two(la_powl(ld, m), h1, h2);
+      if (m != p.span) la_two(ld, m, h1, h2);
       sp[(long long)g * n] = x;
       x = m == 0 ? x : fmaf(h1, x, fmaf(h2, x, own[i]));
     }

@@ -446,3 +446,88 @@ def test_many_steps_keep_the_state(pr):
         a, b = got[0, h].double().cpu().numpy(), want[0, h]
         assert np.linalg.norm(a - b) <= 2.0 ** -17 * np.linalg.norm(b), (
             h, np.linalg.norm(a - b) / np.linalg.norm(b))
+
+
+def same_infinities(got, want, size, f32, F, name):
+    """Non-finite entries are the reference's (NaN where it has NaN, infinities of its
+    sign); the others stay within the bounds of `check`."""
+    got = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want)), name
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf]) and not np.isinf(got[~inf]).any(), name
+    ok = np.isfinite(want)
+    tol = F * size + 1e-30 if f32 else 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + F) * size + 1e-30
+    assert (np.abs(got[ok] - want[ok]) <= tol[ok]).all(), name
+
+
+def infinite(shape, rng):
+    """fp32 states with one infinity of each sign in every head, in different columns."""
+    s = rng.standard_normal(shape).astype(np.float32).astype(float)
+    s[..., 3, 5], s[..., 1, 2] = np.inf, -np.inf
+    return s
+
+
+# gamma: 1, one float alone, two floats, below fp32, none
+INF_DECAYS = np.float32([0.0, -0.4, -1e-3, -0.2, -200.0, -np.inf]).astype(float)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (72, 40), (8, 8)])
+def test_step_keeps_infinite_states(pr, Dk, Dv, dtype):
+    """gamma inf is inf, whatever gamma's parts (0 inf = NaN for gamma = 0 alone)."""
+    H = len(INF_DECAYS)
+    x, _ = make(2, 1, H, H, H, H, Dk, Dv, seed=27)
+    x["log_decay"] = INF_DECAYS
+    x["s0"] = infinite(x["s0"].shape, np.random.default_rng(27))
+    x["v"][1, 0, :, 1] = np.inf             # and an infinite v: k v, in every row
+    x["k"][1] = np.abs(x["k"][1])           # of one sign, so that the output is too
+    x["q"][1] = np.abs(x["q"][1])
+    g = on_gpu(x)
+    o, s = pr.step_linattn(*(g[n][:, 0].to(dtype) for n in "qkv"), g["log_decay"], g["s0"])
+    with np.errstate(invalid="ignore"):
+        wo, ws = ref.scan(**x)
+        ao, as_ = ref.scan(**absolute(x))
+    assert np.isinf(ws).any() and np.isinf(wo).any()
+    same_infinities(s, ws, as_, True, 2.0 ** -22, "s")
+    same_infinities(o[:, None], wo, ao, dtype == torch.float32, 2.0 ** -23 * (Dk + 4), "o")
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("L", [5, 200, 2100])
+def test_scans_keep_infinite_states(pr, form, L):
+    """Both forms, one span and several: an infinite state stays what the recurrence makes
+    of it, to the end and in the gradients that meet it."""
+    H = len(INF_DECAYS)
+    x, y = make(1, L, H, H, H, H, 64, 72, seed=28)
+    rng = np.random.default_rng(28)
+    x["log_decay"] = INF_DECAYS
+    x["s0"], y["ds"] = infinite(x["s0"].shape, rng), infinite(x["s0"].shape, rng)
+    opts = pr.Options(regime=FORMS[form])
+    F = fp32_terms(L, 128)
+    with np.errstate(invalid="ignore"):
+        want, size = ref.scan(**x, scale=0.3), ref.scan(**absolute(x), scale=0.3)
+        grads = ref.backward(**x, **y, scale=0.3)
+        gsize = ref.backward(**absolute(x), **absolute(y), scale=0.3)
+    assert np.isinf(want[1]).any() and np.isinf(grads[3]).any()
+    got = pr.scan_linattn(**on_gpu(x), scale=0.3, opts=opts)
+    for a, w, z, n in zip(got, want, size, ("o", "s")):
+        same_infinities(a, w, z, n == "s", F, n)
+    got = pr.scan_linattn_backward(**on_gpu(x), do=dev(y["do"], BF), ds=dev(y["ds"]), scale=0.3,
+                                   opts=opts)
+    for a, w, z, n in zip(got, grads, gsize, ("dq", "dk", "dv", "ds0")):
+        same_infinities(a, w, z, n == "ds0", F, n)
+
+
+@pytest.mark.parametrize("form", ["recurrent", "chunks"])
+def test_an_infinite_token_leaves_an_infinite_state(pr, form):
+    """A v of one token is infinite: so is the state behind it, in its column alone, over
+    the rest of the prompt and its spans."""
+    x, _ = make(1, 2100, 2, 2, 2, 2, 64, 64, seed=29, state=False)
+    x["log_decay"] = np.array([-0.01, 0.0])
+    x["v"][0, 300, 1, 7] = np.inf
+    with np.errstate(invalid="ignore"):
+        want, size = ref.scan(**x), ref.scan(**absolute(x))
+    assert np.isinf(want[1][0, 1, :, 7]).all()
+    got = pr.scan_linattn(**on_gpu(x), opts=pr.Options(regime=FORMS[form]))
+    for a, w, z, n in zip(got, want, size, ("o", "s")):
+        same_infinities(a, w, z, n == "s", fp32_terms(2100, 64), n)
