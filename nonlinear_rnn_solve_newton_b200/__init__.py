@@ -1002,7 +1002,7 @@ def _apart(outputs, inputs, same=()):
         seen.append((name, lo, hi))
 
 
-def _linattn_apart(d, q, k, v, log_decay, state, out, state_out, name):
+def _linattn_apart(d, q, k, v, log_decay, state, out, state_out, name, lengths=None, status=None):
     """``_apart`` for a forward call, by numbers first: it stands before every decode step."""
     po, ps, pi = out.data_ptr(), state_out.data_ptr(), 0 if state is None else state.data_ptr()
     rows, item = d.B * d.H * d.Dv, out.element_size()
@@ -1010,12 +1010,20 @@ def _linattn_apart(d, q, k, v, log_decay, state, out, state_out, name):
     bq, bk, bv = d.bytes
     apart = not (po < es and ps < eo) and (pi in (0, ps) or not (ps < pi + es - ps and pi < es)) \
         and (pi == 0 or not (po < pi + es - ps and pi < eo))
-    for u, n in ((q.data_ptr(), bq), (k.data_ptr(), bk), (v.data_ptr(), bv),
-                 (log_decay.data_ptr(), 4 * d.H)):
+    reads = [(q.data_ptr(), bq), (k.data_ptr(), bk), (v.data_ptr(), bv),
+             (log_decay.data_ptr(), 4 * d.H)]
+    if lengths is not None:
+        reads.append((lengths.data_ptr(), 4 * d.B))
+    if status is not None:  # written besides: apart from what is read, too
+        reads.append((status.data_ptr(), 4))
+        apart = apart and all(status.data_ptr() + 4 <= u or u + n <= status.data_ptr()
+                              for u, n in reads[:-1] + [(pi, es - ps if pi else 0)])
+    for u, n in reads:
         apart = apart and not (po < u + n and u < eo or ps < u + n and u < es)
     if not apart:
-        _apart((("out", out), ("state_out", state_out)),
-               (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), (name, state)),
+        _apart((("out", out), ("state_out", state_out), ("status", status)),
+               (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), (name, state),
+                ("lengths", lengths)),
                same=(("state_out", name),))
 
 
@@ -1048,8 +1056,8 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
             out = (q.new_empty if lengths is None else q.new_zeros)((B, L, H, Dv))
         if state_out is None:
             state_out = log_decay.new_empty((B, H, Dk, Dv))
-    if given:
-        _linattn_apart(d, q, k, v, log_decay, s0, out, state_out, "s0")
+    if given or status is not None:
+        _linattn_apart(d, q, k, v, log_decay, s0, out, state_out, "s0", lengths, status)
     nws = _linattn_ws(lib, d, 0)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):
@@ -1079,6 +1087,7 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     _check_dev("status", status, torch.int32, (1,))
     dev = _one_device(q=q, k=k, v=v, log_decay=log_decay, do=do, s0=s0, ds=ds, lengths=lengths,
                       status=status)
+    outputs = () if status is None else (("status", status),)
     if out is None:
         with _making_on(stream):
             dq, dk, dv = q.new_empty(q.shape), q.new_empty(k.shape), q.new_empty(v.shape)
@@ -1089,9 +1098,10 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
             _check_dev(name, t, torch.bfloat16, like.shape)
         _check_dev("ds0", ds0, torch.float32, (B, H, Dk, Dv))
         _one_device(q=q, dq=dq, dk=dk, dv=dv, ds0=ds0)
-        _apart((("dq", dq), ("dk", dk), ("dv", dv), ("ds0", ds0)),
-               (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("do", do), ("s0", s0),
-                ("ds", ds), ("lengths", lengths)))
+        outputs += (("dq", dq), ("dk", dk), ("dv", dv), ("ds0", ds0))
+    if outputs:
+        _apart(outputs, (("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("do", do),
+                         ("s0", s0), ("ds", ds), ("lengths", lengths)))
     nws = _linattn_ws(lib, d, 1)
     ws = _call_buffer(nws, dev, stream)
     with _device_guard(dev):

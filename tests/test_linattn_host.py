@@ -329,3 +329,41 @@ def test_layer_norm_refuses_rows_beyond_its_counters():
                                                None, 0, None) == 1
     assert lib.pararnn_layer_norm_workspace_size(2, 1 << 30) > 0
     assert lib.pararnn_layer_norm(p, 0, 8, None, None, p, 0, p, p, 0, 1 << 30, 1e-5, None) == 0
+
+
+def test_outputs_over_lengths_and_status_are_refused(fake):  # noqa: F811
+    # every launch of a scan reads the lengths, and its status word is cleared first and
+    # written last: no output may lie over either, and the word over no input
+    f32, i32 = torch.float32, torch.int32
+    q, k, v, g = qkv(k=z(B, L, H, Dk), v=z(B, L, H, Dk))
+    do, n = dv(z(B, L, H, Dk)), z(B, dtype=i32)
+    st, st2 = (z(B, H, Dk, Dk, dtype=f32) for _ in range(2))
+    out = z(B, L, H, Dk)
+    grads = (*(z(B, L, H, Dk) for _ in range(3)), st2)
+
+    def word(t, at=0, size=1):   # int32s that lie inside a tensor
+        return t.view(-1).view(i32)[at:at + size]
+
+    bad = [
+        lambda: pr.scan_linattn(q, k, v, g, lengths=word(out, 6, B), out=out),
+        lambda: pr.scan_linattn(q, k, v, g, st, lengths=word(st, 30, B), state_out=st),
+        lambda: pr.scan_linattn(q, k, v, g, lengths=n, status=n[1:]),
+        lambda: pr.scan_linattn(q, k, v, g, status=word(g, 2)),
+        lambda: pr.scan_linattn(q, k, v, g, status=word(q, 9)),
+        lambda: pr.scan_linattn(q, k, v, g, st, status=word(st, 100)),
+        lambda: pr.scan_linattn(q, k, v, g, out=out, status=word(out, 3)),
+        lambda: pr.scan_linattn(q, k, v, g, state_out=st, status=word(st, 3)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, lengths=n, status=n[:1]),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, status=word(do, 5)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, s0=st, status=word(st, 5)),
+        lambda: pr.scan_linattn_backward(q, k, v, g, do, out=grads, status=word(st2, 5)),
+    ]
+    for i, call in enumerate(bad):
+        fake.calls.clear()
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+        assert [c for c in fake.calls if "workspace_size" not in c] == [], i
+    two = z(B + 1, dtype=i32)    # neighbours are fine
+    pr.scan_linattn(q, k, v, g, st, lengths=two[:B], out=out, state_out=st, status=two[B:])
+    pr.scan_linattn(q, k, v, g, lengths=two[:B], status=two[B:])
+    pr.scan_linattn_backward(q, k, v, g, do, lengths=two[:B], out=grads, status=two[B:])
