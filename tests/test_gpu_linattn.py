@@ -531,3 +531,69 @@ def test_an_infinite_token_leaves_an_infinite_state(pr, form):
     got = pr.scan_linattn(**on_gpu(x), opts=pr.Options(regime=FORMS[form]))
     for a, w, z, n in zip(got, want, size, ("o", "s")):
         same_infinities(a, w, z, n == "s", fp32_terms(2100, 64), n)
+
+
+# Walks cut into spans of time: few heads, long rows.  (B, L, H, Hq, Hk, Hv, Dk, Dv) and the
+# rows' lengths: whole, within the first span, nothing, at the end of a chunk (and with these
+# sizes of a span), one token beyond.
+SPANS = [((1, 2050, 2, 2, 2, 2, 64, 64), None),
+         ((1, 2200, 3, 1, 3, 1, 128, 72), None),
+         ((1, 2500, 2, 2, 1, 2, 72, 128), None),
+         ((2, 1300, 1, 1, 1, 1, 128, 128), [640, 1300]),
+         ((5, 2300, 2, 2, 1, 2, 64, 64), [2300, 100, 0, 1280, 1281]),
+         ((3, 2300, 2, 1, 2, 2, 128, 72), [768, 2300, 2177]),
+         ((4, 2304, 1, 1, 1, 1, 96, 112), [2304, 0, 384, 129])]
+
+
+def spans_of(pr, g, do):
+    """Spans of the forward walk and of the gradients', from the workspaces they ask for."""
+    d = pr._linattn_desc(g["q"], g["k"], g["v"], g["log_decay"], 1.0, BF, do)
+    state, rows = 4 * d.B * d.H * d.Dk * d.Dv, 4 * d.B * d.L * d.H
+    shared = sum(-(-rows * n // 512) * 512 for n, h in ((d.Dk, d.Hq), (d.Dk, d.Hk), (d.Dv, d.Hv))
+                 if h != d.H)
+    lib = pr.load()
+    return pr._linattn_ws(lib, d, 0) // state, (pr._linattn_ws(lib, d, 1) - shared) // (3 * state)
+
+
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("i", range(len(SPANS)))
+def test_spans(pr, i, state):
+    """Both directions over several spans against the recurrence: states carried over the
+    join, lengths that end inside, before and between spans, heads that are shared."""
+    shape, lengths = SPANS[i]
+    for seed in (31 + i, 34 + i):            # other decays
+        x, y = make(*shape, seed=seed, state=state, lengths=lengths)
+        g, do = on_gpu(x), dev(y["do"], BF)
+        assert min(spans_of(pr, g, do)) > 1
+        B, L, H, Dv = shape[0], shape[1], shape[2], shape[7]
+        for b, n in enumerate(lengths or ()):
+            for t in (g["q"], g["k"], g["v"], do):
+                t[b, n:] = float("nan")
+                t[b, n + 1::2] = float("inf")
+        out = torch.full((B, L, H, Dv), 7.5, dtype=BF, device="cuda")
+        got = pr.scan_linattn(**g, scale=0.4, out=out)
+        for b, n in enumerate(lengths or ()):
+            assert (out[b, n:] == 7.5).all()
+            out[b, n:] = 0
+        check_scan(pr, x, 0.4, got)
+        check_backward(pr, x, y, 0.4, pr.scan_linattn_backward(**g, do=do, ds=dev(y["ds"]), scale=0.4))
+        if state:                            # the state in place: the join reads and writes it
+            s = g["s0"].clone()
+            again = pr.scan_linattn(**dict(g, s0=s), scale=0.4, state_out=s)
+            assert again[1] is s and torch.equal(s, got[1]) and torch.equal(again[0], out)
+
+
+def test_spans_of_strided_views(pr):
+    B, L, H, Hk, Dk, Dv = 1, 2100, 4, 2, 64, 40
+    x, y = make(B, L, H, H, Hk, H, Dk, Dv, seed=38)
+    g, do = on_gpu(x), dev(y["do"], BF)
+    assert min(spans_of(pr, g, do)) > 1
+    pack = torch.cat([g[n].flatten(2) for n in "qkv"], -1)
+    q, k, v = pack.split([H * Dk, Hk * Dk, H * Dv], -1)
+    views = dict(g, q=q.unflatten(-1, (H, Dk)), k=k.unflatten(-1, (Hk, Dk)),
+                 v=v.unflatten(-1, (H, Dv)))
+    got = pr.scan_linattn(**views, scale=0.7)
+    check_scan(pr, x, 0.7, got)
+    assert all(torch.equal(a, b) for a, b in zip(got, pr.scan_linattn(**g, scale=0.7)))
+    grads = pr.scan_linattn_backward(**views, do=do, ds=dev(y["ds"]), scale=0.7)
+    check_backward(pr, x, y, 0.7, grads)
