@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       // ---- tensor copies ----------------------------------------------------------
       const CUtensorMap *mq = &tm.q[blockIdx.z], *mk = &tm.k[blockIdx.z], *mv = &tm.v[blockIdx.z];
       const int hq = h / a.q.rep, hk = h / a.k.rep, hv = h / a.v.rep;
-      int done = 0;  // chunks whose copies were issued
+      int kin = 0, vin = 0;  // chunks whose k, and whose v, were asked for
       for (int c = 0; c < nc + 2 && !*(volatile int*)&s_fail; ++c) {
         const int st = c & 1;
         const unsigned before = (unsigned)((c >> 1) - 1) & 1u;  // parity of chunk c - 2
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           if (!ok) break;
           mbar_expect_tx(&s_vfull[st], kLaBlk);
           tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          vin = c + 1;
         }
         if (c < nc) {
           if (c >= 2) ok = la_wait(&s_kv[st], before, limit);
@@ -448,9 +449,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
           for (int j = 0; j < KD / 64; ++j)
             tma_load_4d_s(sk + j * kLaBlk, mk, 64 * j, t0(c), hk, b, &s_full[st]);
+          kin = c + 1;
           if (FULL) {
             if (c >= 2) ok = la_wait(&s_qs[st], before, limit);
-            if (!ok) break;
+            if (!ok) {
+              mbar_arrive(&s_full[st]);  // in q's place: k alone is waited for below
+              break;
+            }
             mbar_expect_tx(&s_full[st], (KD / 64) * kLaBlk);
 #pragma unroll
             for (int j = 0; j < KD / 64; ++j)
@@ -465,12 +470,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           }
         }
-        if (c < nc) {
-          if (FULL) {
-            mbar_expect_tx(&s_vfull[st], kLaBlk);
-            tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
-          }
-          done = c + 1;
+        if (FULL && c < nc) {
+          mbar_expect_tx(&s_vfull[st], kLaBlk);
+          tma_load_4d_s(sv, mv, col0, t0(c), hv, b, &s_vfull[st]);
+          vin = c + 1;
         }
         if (c + kLaAhead < nc) {
           const int t = t0(c + kLaAhead);
@@ -482,15 +485,15 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           tma_prefetch_4d(mv, col0, t, hv, b);
         }
       }
-      if (done < nc) s_fail = 1;
-      // no copy is in flight when the CTA exits (only a failed wait leaves loads; a k or
-      // v without its q is waited for too, in vain where it was never issued)
+      if (kin < nc || vin < nc) s_fail = 1;
+      // no copy is in flight when the CTA exits (only a failed wait leaves loads, of the last
+      // two chunks)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       const long long last = limit < 2000000000LL ? 2000000000LL : limit;
-      for (int i = done - 2 < 0 ? 0 : done - 2; i < (done < nc ? done + 1 : done); ++i) {
+      for (int i = kin < 2 ? 0 : kin - 2; i < kin; ++i)
         la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
+      for (int i = vin < 2 ? 0 : vin - 2; i < vin; ++i)
         la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
-      }
     }
   } else if (warp == 1) {
     // ---- products -----------------------------------------------------------------

@@ -597,3 +597,20 @@ def test_spans_of_strided_views(pr):
     assert all(torch.equal(a, b) for a, b in zip(got, pr.scan_linattn(**g, scale=0.7)))
     grads = pr.scan_linattn_backward(**views, do=do, ds=dev(y["ds"]), scale=0.7)
     check_backward(pr, x, y, 0.7, grads)
+
+
+@pytest.mark.parametrize("L", [300, 2050])
+def test_a_wait_that_ran_out_does_not_hold_the_gpu(pr, L):
+    """Where a wait runs out, the CTA waits for the copies that it asked for and for no
+    others: a call ends in far less than the two seconds that each such wait may take."""
+    x, y = make(1, L, 2, 2, 1, 2, 128, 64, seed=39)
+    g, do, ds = on_gpu(x), dev(y["do"], BF), dev(y["ds"])
+    opts = pr.Options(regime=2, wait_timeout_ns=1)
+    ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    torch.cuda.synchronize()
+    ends[0].record()
+    pr.scan_linattn(**g, opts=opts)
+    pr.scan_linattn_backward(**g, do=do, ds=ds, opts=opts)
+    ends[1].record()
+    torch.cuda.synchronize()
+    assert ends[0].elapsed_time(ends[1]) < 1000
