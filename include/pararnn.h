@@ -468,7 +468,8 @@ size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* desc, int32_t bac
  *  o [B, L, H, Dv] bf16.   s [B, H, Dk, Dv] fp32: the state after the last token,
  *  or NULL; s may be s0 itself.
  *  ws, ws_bytes: workspace of pararnn_linattn_workspace_size(desc, 0) bytes.
- *  status_dev: optional device int32 for the device-side status.
+ *  status_dev: optional device int32 for the device-side status: 0, or 4 (timeout) where a
+ *  wait of the chunked form ran out; the outputs are then undefined.
  *  opts->regime chooses the form: 0 automatic (recurrent up to 8 tokens), 1 recurrent
  *  (fp32 arithmetic, a token at a time), 2 chunks of 128 tokens on the tensor cores.
  *  Only regime and wait_timeout_ns of opts are read.

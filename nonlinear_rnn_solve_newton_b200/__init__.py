@@ -1037,7 +1037,9 @@ def scan_linattn(q, k, v, log_decay, s0=None, scale=1.0, lengths=None, out=None,
     (o [B, L, H, Dv] bf16, s [B, H, Dk, Dv] fp32).  lengths [B] int32 (device): tokens
     at and after a row's length are not used; their rows of o are left as they were
     in ``out`` and are zero in a tensor this call makes.  ``state_out`` may be s0; outputs
-    lie over no other argument."""
+    lie over no other argument.  ``status`` [1] int32 (device) is 0, or 4 where a wait on the
+    device ran out (``opts.wait_timeout_ns``): the results are then undefined.  Nothing is
+    raised for that, the call does not wait for the device."""
     lib = load()
     if q.dim() != 4:
         raise ValueError("q, k, v must be [B, L, heads, size]")
@@ -1075,7 +1077,8 @@ def scan_linattn_backward(q, k, v, log_decay, do, s0=None, ds=None, scale=1.0, l
     """Gradients of a loss through ``scan_linattn``, given do = dl/do [B, L, H, Dv] bf16
     and ds = dl/ds of the final state (or None): (dq, dk, dv bf16 in the shapes of q, k
     and v, summed over the heads that share one; ds0 [B, H, Dk, Dv] fp32).  Rows at and
-    after a batch row's length get zeros.  The decay is a constant of the layer."""
+    after a batch row's length get zeros.  The decay is a constant of the layer.  Outputs lie
+    over no other argument; ``status`` as in ``scan_linattn``."""
     lib = load()
     if q.dim() != 4 or do.dim() != 4:
         raise ValueError("q, k, v and do must be [B, L, heads, size]")

@@ -426,13 +426,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const CUtensorMap *mq = &tm.q[blockIdx.z], *mk = &tm.k[blockIdx.z], *mv = &tm.v[blockIdx.z];
       const int hq = h / a.q.rep, hk = h / a.k.rep, hv = h / a.v.rep;
       int kin = 0, vin = 0;  // chunks whose k, and whose v, were asked for
+      bool ok = true;
       for (int c = 0; c < nc + 2 && !*(volatile int*)&s_fail; ++c) {
         const int st = c & 1;
         const unsigned before = (unsigned)((c >> 1) - 1) & 1u;  // parity of chunk c - 2
         const unsigned sk = sbase + Sm::kK + st * (KD / 64) * kLaBlk,
                        sq = sbase + Sm::kQ + st * (KD / 64) * kLaBlk,
                        sv = sbase + Sm::kV + st * kLaBlk;
-        bool ok = true;
         // each buffer as soon as chunk c - 2 has no more use for it: k, q, then v, where
         // that chunk's output is staged
         if (!FULL && c < nc) {  // v is of no use once it has been weighted
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           tma_prefetch_4d(mv, col0, t, hv, b);
         }
       }
-      if (kin < nc || vin < nc) s_fail = 1;
+      if (!ok) s_fail = 1;  // also where only the last outputs are not stored
       // no copy is in flight when the CTA exits (only a failed wait leaves loads, of the last
       // two chunks)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");

@@ -614,3 +614,25 @@ def test_a_wait_that_ran_out_does_not_hold_the_gpu(pr, L):
     ends[1].record()
     torch.cuda.synchronize()
     assert ends[0].elapsed_time(ends[1]) < 1000
+
+
+@pytest.mark.parametrize("L", [300, 2050])
+def test_waits_that_run_out(pr, L):
+    """Waits of a few microseconds end in the status word: where it says 0 the call has done all
+    of its work.  A call after it is right.  One span, and several."""
+    x, y = make(1, L, 2, 2, 1, 2, 128, 64, seed=39)
+    g, do, ds = on_gpu(x), dev(y["do"], BF), dev(y["ds"])
+    want = (*pr.scan_linattn(**g), *pr.scan_linattn_backward(**g, do=do, ds=ds))
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for limit in (1, 2000, 4000, 8000, 16000) * 8:
+        opts = pr.Options(regime=2, wait_timeout_ns=limit)
+        got = pr.scan_linattn(**g, opts=opts, status=status[:1])
+        got += pr.scan_linattn_backward(**g, do=do, ds=ds, opts=opts, status=status[1:])
+        words = status.tolist()
+        assert set(words) <= {0, 4}
+        for w, a, b in ((words[0], want[:2], got[:2]), (words[1], want[2:], got[2:])):
+            assert w == 4 or all(torch.equal(p, q) for p, q in zip(a, b))
+    again = pr.scan_linattn(**g, status=status[:1])
+    again += pr.scan_linattn_backward(**g, do=do, ds=ds, status=status[1:])
+    assert status.tolist() == [0, 0]
+    assert all(torch.equal(p, q) for p, q in zip(want, again))
