@@ -2,19 +2,23 @@
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import re
 import shutil
 import subprocess
 import sys
+import time
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpararnn.so")
+BUILD = os.path.join(HERE, "_build")  # objects, kept for the next build
 SOURCES = [os.path.join(CSRC, f) for f in ("pararnn.cu", "linattn.cu", "norm.cu")]
-DEPS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "pararnn.h")]
+DEPS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
+    os.path.join(INCLUDE, "pararnn.h"), os.path.abspath(__file__)]
 
 
 def nvcc_path() -> str:
@@ -45,26 +49,44 @@ def _includes(path, seen=None):
     return seen
 
 
-def _object(src):
-    return os.path.join(HERE, "_build", os.path.basename(src) + ".o")
+def _flags():
+    return ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+            "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
+
+
+def _settings(flags):
+    """A name for what makes an object besides its sources: the flags and the compiler."""
+    version = subprocess.run([nvcc_path(), "--version"], capture_output=True, check=True).stdout
+    return hashlib.sha256(repr(flags).encode() + version).hexdigest()[:12]
+
+
+def _object(src, settings):
+    return os.path.join(BUILD, f"{os.path.basename(src)}.{settings}.o")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
-    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-             "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
-    if verbose:
-        flags.insert(0, "-Xptxas=-v")
-    os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
+    # Results are as old as the start of the build that made them: a source edited while it
+    # is compiled is newer, and compiled again.
+    started = time.time_ns()
+    own = f".{os.getpid()}.tmp"  # two processes may build at once
+    flags = _flags()
+    settings = _settings(flags)
+
+    def put(path):
+        os.utime(path + own, ns=(started, started))
+        os.replace(path + own, path)
+
+    os.makedirs(BUILD, exist_ok=True)
     jobs = []
     for src in SOURCES:  # the sources that changed, side by side
-        obj = _object(src)
+        obj = _object(src, settings)
         if not force and os.path.exists(obj):
             t = os.path.getmtime(obj)
             if all(os.path.getmtime(p) <= t for p in _includes(src)):
                 continue
-        cmd = [nvcc_path(), *flags, "-c", src, "-o", obj + ".tmp"]
+        cmd = [nvcc_path(), *(["-Xptxas=-v"] if verbose else []), *flags, "-c", src, "-o", obj + own]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         jobs.append((cmd, obj, subprocess.Popen(cmd)))
@@ -72,14 +94,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for cmd, obj, job in jobs:
         rc = job.wait()
         if rc == 0:
-            os.replace(obj + ".tmp", obj)
+            put(obj)
         else:
             failed = failed or subprocess.CalledProcessError(rc, cmd)
     if failed:
         raise failed
     subprocess.check_call([nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared",
-                           *[_object(s) for s in SOURCES], "-o", LIB + ".tmp"])
-    os.replace(LIB + ".tmp", LIB)
+                           *[_object(s, settings) for s in SOURCES], "-o", LIB + own])
+    put(LIB)
     return LIB
 
 
