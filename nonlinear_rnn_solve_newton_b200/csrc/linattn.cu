@@ -300,7 +300,8 @@ extern "C" pararnn_status_t pararnn_scan_linattn(const pararnn_linattn_t* d, con
         !la_aligned(log_decay, 4) || !la_aligned(lengths, 4))
       return PARARNN_ERR_INVALID_ARGUMENT;
   }
-  if (!la_aligned(s0, 16) || !la_aligned(s, 16)) return PARARNN_ERR_INVALID_ARGUMENT;
+  if (!la_aligned(s0, 16) || !la_aligned(s, 16) || !la_aligned(status_dev, 4))
+    return PARARNN_ERR_INVALID_ARGUMENT;
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
   const LaPlan pl = la_plan(d, false, opts);
   const LaWs w = la_ws(d, false, pl);
@@ -356,7 +357,8 @@ extern "C" pararnn_status_t pararnn_scan_linattn_backward(
       if (!la_aligned(x, 16)) return PARARNN_ERR_INVALID_ARGUMENT;
     if (!la_aligned(log_decay, 4) || !la_aligned(lengths, 4)) return PARARNN_ERR_INVALID_ARGUMENT;
   }
-  if (!la_aligned(s0, 16) || !la_aligned(ds, 16) || !la_aligned(ds0, 16) || (ds && ds == ds0))
+  if (!la_aligned(s0, 16) || !la_aligned(ds, 16) || !la_aligned(ds0, 16) || (ds && ds == ds0) ||
+      !la_aligned(status_dev, 4))
     return PARARNN_ERR_INVALID_ARGUMENT;
   if (opts && (opts->regime < 0 || opts->regime > 2)) return PARARNN_ERR_INVALID_ARGUMENT;
   const LaPlan pl = la_plan(d, true, opts);

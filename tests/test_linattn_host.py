@@ -367,3 +367,14 @@ def test_outputs_over_lengths_and_status_are_refused(fake):  # noqa: F811
     pr.scan_linattn(q, k, v, g, st, lengths=two[:B], out=out, state_out=st, status=two[B:])
     pr.scan_linattn(q, k, v, g, lengths=two[:B], status=two[B:])
     pr.scan_linattn_backward(q, k, v, g, do, lengths=two[:B], out=grads, status=two[B:])
+
+
+def test_status_words_off_their_alignment_are_refused():
+    # the kernels set the word by an atomic, which faults at such an address
+    lib = pr.load()
+    vp = ctypes.c_void_p
+    d, p, ws, odd = _desc(), vp(4096), vp(1 << 20), vp(4098)
+    assert lib.pararnn_scan_linattn(ctypes.byref(d), p, p, p, p, None, None, p, p, ws, 1 << 40, odd,
+                                    None, None) == 1
+    assert lib.pararnn_scan_linattn_backward(ctypes.byref(d), p, p, p, p, None, p, None, None, p, p,
+                                             p, p, ws, 1 << 40, odd, None, None) == 1
