@@ -486,14 +486,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       if (!ok) s_fail = 1;  // also where only the last outputs are not stored
-      // no copy is in flight when the CTA exits (only a failed wait leaves loads, of the last
-      // two chunks)
+      // no copy is in flight when the CTA exits: the last output has been read, and behind it
+      // all loads were; the loads of the last two chunks are waited for where there is none
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      const long long last = limit < 2000000000LL ? 2000000000LL : limit;
-      for (int i = kin < 2 ? 0 : kin - 2; i < kin; ++i)
-        la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
-      for (int i = vin < 2 ? 0 : vin - 2; i < vin; ++i)
-        la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
+      if (!FULL || *(volatile int*)&s_fail) {
+        const long long last = limit < 2000000000LL ? 2000000000LL : limit;
+        for (int i = kin < 2 ? 0 : kin - 2; i < kin; ++i)
+          la_wait(&s_full[i & 1], (unsigned)(i >> 1) & 1u, last);
+        for (int i = vin < 2 ? 0 : vin - 2; i < vin; ++i)
+          la_wait(&s_vfull[i & 1], (unsigned)(i >> 1) & 1u, last);
+      }
     }
   } else if (warp == 1) {
     // ---- products -----------------------------------------------------------------
