@@ -636,3 +636,25 @@ def test_waits_that_run_out(pr, L):
     again += pr.scan_linattn_backward(**g, do=do, ds=ds, status=status[1:])
     assert status.tolist() == [0, 0]
     assert all(torch.equal(p, q) for p, q in zip(want, again))
+
+
+@pytest.mark.parametrize("L", [6, 200, 2050])
+def test_growing_heads(pr, L):
+    """gamma above 1 (a positive log decay) within the range of fp32: one token at a time, one
+    span and several.  The bounds go by the sums of sizes, which grow with the state."""
+    x, y = make(1, L, 2, 2, 2, 2, 64, 64, seed=40)
+    x["log_decay"] = np.float32([0.02, 0.001]).astype(float)
+    g = on_gpu(x)
+    check_scan(pr, x, 0.3, pr.scan_linattn(**g, scale=0.3))
+    check_backward(pr, x, y, 0.3, pr.scan_linattn_backward(**g, do=dev(y["do"], BF),
+                                                           ds=dev(y["ds"]), scale=0.3))
+
+
+def test_one_tensor_as_several_streams(pr):
+    x, y = make(2, 150, 3, 3, 3, 3, 64, 64, seed=41)
+    x["k"] = x["v"] = x["q"]
+    g = on_gpu(x)
+    g["k"] = g["v"] = g["q"]
+    check_scan(pr, x, 0.3, pr.scan_linattn(**g, scale=0.3))
+    y["do"] = x["q"]
+    check_backward(pr, x, y, 0.3, pr.scan_linattn_backward(**g, do=g["q"], ds=dev(y["ds"]), scale=0.3))

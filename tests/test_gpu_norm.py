@@ -216,3 +216,15 @@ def test_one_row_longer_than_registers(pr, D, off, tx, ty):
     dy = ref.bf16(dy) if ty == BF else dy.astype(np.float32).astype(float)
     grads = pr.layer_norm_backward(dev(dy, ty), X, got[1], got[2], dev(w))
     check_backward(dy, x, host(got[1]), host(got[2]), w, grads, tx)
+
+
+@pytest.mark.parametrize("size", [(100000, 1), (70000, 8), (40000, 3)])
+def test_many_short_rows(pr, size):
+    x, w, b, rng = make(*size, 28, F32)
+    if size[1] == 1:
+        x = x * 0 + 0.5                  # a row of one is its own mean: y is the bias
+    got = pr.layer_norm(dev(x), dev(w), dev(b))
+    check_forward(x, w, b, got, F32)
+    dy = rng.standard_normal(size).astype(np.float32).astype(float)
+    grads = pr.layer_norm_backward(dev(dy), dev(x), got[1], got[2], dev(w))
+    check_backward(dy, x, host(got[1]), host(got[2]), w, grads, F32)
