@@ -470,8 +470,10 @@ size_t pararnn_linattn_workspace_size(const pararnn_linattn_t* desc, int32_t bac
  *  ws, ws_bytes: workspace of pararnn_linattn_workspace_size(desc, 0) bytes.
  *  status_dev: optional device int32 for the device-side status: 0, or 4 (timeout) where a
  *  wait of the chunked form ran out; the outputs are then undefined.
- *  opts->regime chooses the form: 0 automatic (recurrent up to 8 tokens), 1 recurrent
- *  (fp32 arithmetic, a token at a time), 2 chunks of 128 tokens on the tensor cores.
+ *  opts->regime chooses the form: 0 automatic (recurrent up to 8 tokens, chunks beyond), 1
+ *  recurrent (fp32 arithmetic, a token at a time), 2 chunks of 128 tokens on the tensor
+ *  cores.  Chunks round two operands of o's products to bf16, the weighted scores and the
+ *  state that q multiplies (each term by at most 2^-8); states are fp32 in both forms.
  *  Only regime and wait_timeout_ns of opts are read.
  * Outputs must not overlap inputs or each other, but for s and s0.
  * A token that is not finite changes nothing before it; where one occurs, or a product

@@ -53,7 +53,8 @@
 // for good, so the end of the walk shows it.  A product q.k beyond fp32 shows in the
 // weighted scores, whose largest is kept (also where v is zero or the token later,
 // so that no output should see it).  In both cases the CTA walks its tokens again with
-// the recurrent form, which reads no token before its time and makes no scores.
+// the recurrent form, which reads no token before its time and makes no scores; in the walk
+// of the states only, so that a span leaves the infinities that the recurrence has there.
 //
 // Spans: where (batch row, head, tile) give fewer CTAs than SMs, time is cut into
 // spans.  A first launch (FULL = false) computes the state that each span's own
