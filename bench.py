@@ -262,16 +262,24 @@ def projection_bytes(M, N, K, out_bf16):
     return 2 * M * K + 2 * N * K + 4 * N + (2 if out_bf16 else 4) * M * N
 
 
+def kernel_sources():
+    """The CUDA sources that the workloads' kernels are made from: pararnn.cu and what it
+    includes (other operators of the library have sources of their own)."""
+    from nonlinear_rnn_solve_newton_b200 import build
+
+    return sorted(p for p in build._includes(os.path.join(build.CSRC, "pararnn.cu"))
+                  if os.path.dirname(p) == build.CSRC)
+
+
 def kernel_source_digest():
-    """sha256 of the CUDA sources: ties a recorded ncu traffic figure to the
-    kernel it was measured on."""
+    """sha256 of those sources: ties a recorded ncu traffic figure to the kernel it was
+    measured on."""
     import hashlib
 
     hsh = hashlib.sha256()
-    csrc = os.path.join(ROOT, "nonlinear_rnn_solve_newton_b200", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        with open(os.path.join(csrc, name), "rb") as f:
-            hsh.update(name.encode() + b"\0" + f.read())
+    for path in kernel_sources():
+        with open(path, "rb") as f:
+            hsh.update(os.path.basename(path).encode() + b"\0" + f.read())
     return hsh.hexdigest()
 
 

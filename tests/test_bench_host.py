@@ -1,6 +1,8 @@
 """Host-side arithmetic of bench.py (CPU only): the algorithmic bytes and MUFU
 operation counts that the roofline figures divide by, and the sweep schedule
 the kernels follow."""
+import os
+
 import bench
 
 
@@ -115,3 +117,11 @@ def test_cpu_baseline_projected_solve():
     out = bench.cpu_baseline(x, "proj_solve", 1, 64, 16, budget_s=0.05)
     assert out["kind"] == "oracle" and out["value"] > 0 and out["cores"] >= 1
     assert "projection" in out["sample"]
+
+
+def test_traffic_records_outlive_other_operators():
+    """The digest covers the sources of the workloads' kernels and no others: a change of
+    linear attention or layer norm does not unmeasure the solves."""
+    names = {os.path.basename(p) for p in bench.kernel_sources()}
+    assert {"pararnn.cu", "pararnn_kernel.cuh", "pararnn_proj.cuh", "pararnn_seq.cuh"} <= names
+    assert not any("linattn" in n or "norm" in n for n in names)
