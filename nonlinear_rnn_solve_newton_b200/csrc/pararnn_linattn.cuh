@@ -89,14 +89,19 @@ __device__ __forceinline__ double la_pow(float log_decay, int i) { return la_pow
 // (0 inf or inf - inf would be NaN).  The least value, 2^-149, is far below every rounding of a
 // normal hi; a smaller gamma^i becomes twice that.
 constexpr float kLaLeast = 1.40129846e-45f;
-__device__ __forceinline__ void la_two(float log_decay, long long i, float& hi, float& lo) {
-  const double x = la_powl(log_decay, i);
-  hi = __double2float_rz(x);
-  lo = (float)(x - (double)hi);
+__device__ __noinline__ inline float2 la_two(float log_decay, long long i) {
+  const double x = exp((double)log_decay * (double)i);
+  float hi = __double2float_rz(x), lo = (float)(x - (double)hi);
   if (log_decay > -INFINITY) {
     hi = fmaxf(hi, kLaLeast);
     lo = fmaxf(lo, kLaLeast);
   }
+  return make_float2(hi, lo);
+}
+__device__ __forceinline__ void la_two(float log_decay, long long i, float& hi, float& lo) {
+  const float2 two = la_two(log_decay, i);
+  hi = two.x;
+  lo = two.y;
 }
 
 // ---------------------------------------------------------------------------
